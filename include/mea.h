@@ -322,6 +322,150 @@ int mea_bwd_stages(const void* q, const void* k, const void* v, const void* out,
                    int alibi, float scale, void* workspace, size_t workspace_bytes,
                    int stages, cudaStream_t stream);
 
+/*
+ * The 4-bit cache.  A decode step is bound by reading the cache ("Transformer :
+ * comprendre l'entrainement et l'inference", section "Pre-remplissage et
+ * decodage"); held in 4 bits, a row of K dimensions takes K/2 + K/16 bytes
+ * instead of 2 K.  Four planes, each contiguous, with head-major rows:
+ *   k_codes, v_codes    uint8 [B, Hkv, cache_rows, K/2]: dimension d in byte d/2,
+ *                       even d in the low four bits
+ *   k_params, v_params  16-bit [B, Hkv, cache_rows, K/64, 2]: the step s and the
+ *                       zero z of each group of 64 dimensions, in the type
+ *                       (MEA_F16 / MEA_BF16) of the rows that were stored
+ * and a code c stands for z + s c.  z is the group's least value, s its range / 15
+ * (computed in fp32, rounded to the 16-bit type), c the nearest integer to
+ * (x - z) / s, ties to even, held to 0..15; a group of equal values has s = 0 and
+ * c = 0.  A group that holds a NaN or an infinity stands for NaN throughout.
+ *
+ * mea_kv4_append -- puts n = q_seqlens[b] (M if NULL) new rows of every sequence
+ * after its past = cache_seqlens[b] rows, as mea_prefill_chunk does for a 16-bit
+ * cache: rows [past, past + n) of all four planes are written, nothing else.
+ *   k_new, v_new  [B, M, Hkv, K] element strides (b, m, h), K contiguous; rows >= n unused
+ *   cache_seqlens DEVICE int32 [B], not updated (the caller adds n afterwards)
+ * A sequence with past < 0, n outside [0, M] or past + n > cache_rows is skipped
+ * and records MEA_ERR_INVALID_ARG in the device status word.
+ */
+int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_params,
+                   void* v_codes, void* v_params, const int32_t* cache_seqlens,
+                   const int32_t* q_seqlens, int B, int M, int cache_rows, int Hkv, int K,
+                   const int64_t kn_strides[3], const int64_t vn_strides[3], mea_dtype_t dtype,
+                   cudaStream_t stream);
+
+/*
+ * mea_kv4_read -- rows of a 4-bit cache as 16-bit rows (what the codes stand for,
+ * rounded once), for the operations that take 16-bit keys and values: the history
+ * in front of a chunk of prefill, for instance.  For r < rows[b]:
+ *     k_out[b, r] = cache row first_rows[b] + r (from row 0 if first_rows is NULL)
+ *   k_out, v_out  [B, out_rows, Hkv, K] element strides (b, row, h), K contiguous;
+ *                 rows >= rows[b] are not written
+ *   rows, first_rows  DEVICE int32 [B]; rows[b] outside [0, out_rows] or a range
+ *                 outside the cache: the sequence is skipped, MEA_ERR_INVALID_ARG
+ *                 in the device status word.
+ * `dtype` is the type the rows were stored with.
+ */
+int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
+                 const void* v_params, const int32_t* rows, const int32_t* first_rows,
+                 void* k_out, void* v_out, int B, int cache_rows, int out_rows, int Hkv, int K,
+                 const int64_t ko_strides[3], const int64_t vo_strides[3], mea_dtype_t dtype,
+                 cudaStream_t stream);
+
+/*
+ * mea_decode_kv4 -- mea_decode on a 4-bit cache: a single new query per sequence
+ * against rows [0, kv_seqlens[b]) of its slot (the new token's row already
+ * appended), with the values the codes stand for; no value of the cache is rounded
+ * again on the way.
+ *   q, out       [B, Hq, K] contiguous, dtype (the type the cache was stored with)
+ *   lse          [B, Hq] fp32 natural log, or NULL
+ *   kv_seqlens   DEVICE int32 [B]
+ *   max_kv_len   host-known upper bound on every kv_seqlens[b] (sizes the split grid)
+ *   weights_out  [B, Hkv, cache_rows] fp32 or NULL: the weight every row has gathered,
+ *                weights_out[b, h, j] = weights_in[b, h, j] + sum of softmax weights of
+ *                row j over the query heads of kv head h, for j < kv_seqlens[b], and 0
+ *                for the rows after them
+ *   weights_in   the same layout, may be weights_out itself; NULL counts as zeros
+ * Any group size Hq / Hkv.  ALiBi as in mea_decode (position = row number).  An empty
+ * sequence gives out = 0, lse = -inf.  A sequence whose length is negative or above
+ * min(max_kv_len, cache_rows) gets out = 0 and lse = NaN, its weights_out is left as
+ * it was, and the device status word records MEA_ERR_INVALID_ARG.
+ *
+ * workspace: DEVICE scratch of at least mea_decode_kv4_workspace_size(...) bytes
+ * (weights: nonzero if weights_out is given), 256-byte aligned, contents irrelevant;
+ * may be NULL if that size is 0.  Calls that share a workspace must not overlap.
+ */
+size_t mea_decode_kv4_workspace_size(int B, int Hq, int Hkv, int K, int max_kv_len, int weights);
+
+int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                   const void* v_params, const int32_t* kv_seqlens, void* out, float* lse,
+                   const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int K,
+                   int cache_rows, int max_kv_len, mea_dtype_t dtype, int alibi, float scale,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * mea_key_weights -- the attention weight that each key gathers from a set of
+ * queries, from the log-sum-exp their attention returned (the weights are
+ * recomputed as in mea_bwd and summed over the queries):
+ *     weights_out[b, h, j] = weights_in[b, h, j]
+ *         + sum over query heads g of kv head h, rows i < n that see key j
+ *           of exp(scale q[b,i,g].k[b,j,h] + b_ij - lse[b,g,i])
+ *   q    [B, M, Hq, K], k [B, N, Hkv, K]  element strides (b, row, h), K contiguous
+ *   lse  [B, Hq, M] fp32 natural log, as written by mea_fwd (bias none or causal) or
+ *        mea_prefill_chunk for the same q, scale and alibi; a row with lse = -inf adds
+ *        nothing
+ *   cache_seqlens, q_seqlens  DEVICE int32 [B] as given to mea_prefill_chunk (the rows
+ *        before the chunk, and the chunk's real rows, M if NULL): row i sits at position
+ *        past + i and key rows [0, past + n) take part.  cache_seqlens NULL: all N keys
+ *        take part and past = N - M (mea_fwd); q_seqlens must then be NULL.
+ *   causal  0 or 1: row i sees keys j <= past + i
+ *   weights_in, weights_out  [B, Hkv, N] fp32 contiguous; weights_in may be weights_out
+ *        itself, NULL counts as zeros.  Rows past + n and later get 0.
+ * A sequence with past < 0, n outside [0, M] or past + n > N is skipped (weights_out
+ * left as it was) and records MEA_ERR_INVALID_ARG in the device status word; a bounded
+ * wait that gives up records MEA_ERR_DEVICE_TIMEOUT and leaves NaN in its keys' weights.
+ * The same call gives the same bits every time.  scale must be >= 0 and K 64 or 128;
+ * for M = 0 pass cache_seqlens.
+ */
+int mea_key_weights(const void* q, const void* k, const float* lse, const int32_t* cache_seqlens,
+                    const int32_t* q_seqlens, const float* weights_in, float* weights_out, int B,
+                    int M, int N, int Hq, int Hkv, int K, const int64_t q_strides[3],
+                    const int64_t k_strides[3], mea_dtype_t dtype, int causal, int alibi,
+                    float scale, cudaStream_t stream);
+
+/*
+ * mea_cache_evict -- cuts every sequence of a cache down to `budget` rows by the
+ * weight its rows have gathered, per kv head: of n = cache_seqlens[b] > budget rows
+ * the newest `recent` stay, and of the others the budget - recent heaviest (equal
+ * weights: the lowest row first; a NaN weighs least).  The kept rows move to rows
+ * [0, budget) in their old order, in every plane and in the weights.  A sequence of
+ * n <= budget keeps all its rows.
+ *   planes       1 to 4 arrays of rows (keys, values; codes and params of a 4-bit
+ *                cache), byte strides (b, row, h); row_bytes a multiple of 4, as must
+ *                be pointers and strides (MEA_ERR_UNSUPPORTED)
+ *   weights      [B, Hkv, cache_rows] fp32
+ *   weights_out  [B, Hkv, out_rows] fp32: the kept rows' weights, 0 after them
+ *   cache_seqlens  DEVICE int32 [B]
+ *   new_seqlens  DEVICE int32 [B], written: min(n, budget); must not be cache_seqlens
+ *   kept         DEVICE int32 [B, Hkv, budget], written: old row of each kept row, -1
+ *                after the last
+ * In place: dst == src with the same strides, weights_out == weights, out_rows ==
+ * cache_rows; or into other memory: no destination may overlap a source otherwise
+ * (MEA_ERR_INVALID_ARG).  out_rows >= budget >= 1, 0 <= recent <= budget.  Destination
+ * rows past the kept ones are left as they were.  A sequence with n outside
+ * [0, cache_rows] is not moved: new_seqlens 0, kept -1, MEA_ERR_INVALID_ARG in the
+ * device status word.
+ */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_strides[3]; /* bytes: b, row, head */
+  int64_t dst_strides[3];
+  int32_t row_bytes;
+} mea_plane_t;
+
+int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weights,
+                    float* weights_out, const int32_t* cache_seqlens, int32_t* new_seqlens,
+                    int32_t* kept, int B, int Hkv, int cache_rows, int out_rows, int budget,
+                    int recent, cudaStream_t stream);
+
 /* Number of key/value rows one decode split covers (the unit of parallelism). */
 int mea_decode_chunk(void);
 

@@ -12,16 +12,23 @@ Operations (sources cited in ``include/mea.h``):
   mea_prefill_chunk  a chunk of new queries against a KV cache, appending its keys/values.
   mea_bwd     dq, dk, dv by recomputing the weights from the forward's lse.
   mea_decode  one query per sequence against a packed, ragged KV cache.
+  mea_kv4_append, mea_kv4_read, mea_decode_kv4  a KV cache held in 4 bits: rows put
+              into it, rows read back in 16 bits, one decode step against it.
+  mea_key_weights  the attention weight each key gathered, from q, k and the lse.
+  mea_cache_evict  a cache cut down to its newest and heaviest rows.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["mea_fwd", "mea_fwd_block_sparse", "mea_prefill_chunk", "mea_bwd", "mea_decode",
-           "mea_decode_workspace_size", "mea_decode_chunk", "read_device_status", "status_string",
+           "mea_decode_workspace_size", "mea_decode_chunk", "Kv4Cache", "mea_kv4_alloc",
+           "mea_kv4_append", "mea_kv4_read", "mea_decode_kv4", "mea_decode_kv4_workspace_size",
+           "mea_key_weights", "mea_cache_evict", "read_device_status", "status_string",
            "MeaError", "PreparedCall", "BIAS", "BWD_PREP", "BWD_MAIN", "BWD_DQ", "LIB_PATH", "lib"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmea.so")
@@ -30,6 +37,11 @@ BIAS = {"none": 0, "causal": 1, "blockdiag": 2, "blockdiag_causal": 3}
 BWD_PREP, BWD_MAIN, BWD_DQ = 1, 2, 4  # stages of the backward (mea_bwd_stages)
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1}
 _i64x3 = ctypes.c_int64 * 3
+
+
+class _Plane(ctypes.Structure):  # mea_plane_t
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_strides", _i64x3),
+                ("dst_strides", _i64x3), ("row_bytes", ctypes.c_int32)]
 
 
 class MeaError(RuntimeError):
@@ -66,6 +78,18 @@ def _load() -> ctypes.CDLL:
     L.mea_bwd.argtypes = [vp] * 9 + [i] * 8 + [vp, vp, i, i, i, i, f, vp, sz, vp]
     L.mea_bwd_stages.restype = i
     L.mea_bwd_stages.argtypes = [vp] * 9 + [i] * 8 + [vp, vp, i, i, i, i, f, vp, sz, i, vp]
+    L.mea_kv4_append.restype = i
+    L.mea_kv4_append.argtypes = [vp] * 8 + [i] * 5 + [vp, vp, i, vp]
+    L.mea_kv4_read.restype = i
+    L.mea_kv4_read.argtypes = [vp] * 8 + [i] * 5 + [vp, vp, i, vp]
+    L.mea_decode_kv4_workspace_size.restype = sz
+    L.mea_decode_kv4_workspace_size.argtypes = [i] * 6
+    L.mea_decode_kv4.restype = i
+    L.mea_decode_kv4.argtypes = [vp] * 10 + [i] * 8 + [f, vp, sz, vp]
+    L.mea_key_weights.restype = i
+    L.mea_key_weights.argtypes = [vp] * 7 + [i] * 6 + [vp, vp, i, i, i, f, vp]
+    L.mea_cache_evict.restype = i
+    L.mea_cache_evict.argtypes = [ctypes.POINTER(_Plane), i] + [vp] * 5 + [i] * 6 + [vp]
     L.mea_decode_chunk.restype = i
     L.mea_decode_chunk.argtypes = []
     L.mea_status_string.restype = ctypes.c_char_p
@@ -405,6 +429,314 @@ def mea_decode(q, k_cache, v_cache, kv_seqstart, max_kv_len: int, scale: float |
                         int(bool(alibi)), scale, _ptr(workspace), ws_bytes, _stream(stream, q.device))
     _check("mea_decode", rc)
     return out, lse
+
+
+def _launch(name, fn, device, stream, scratch, args):
+    """Runs fn(*args, stream) with `device` current.  `scratch` are the tensors this
+    call allocated: on a stream that is not the one they were allocated for, their
+    memory may not be handed out again before the call has run."""
+    other = device.index is not None and device.index != torch.cuda.current_device()
+    with torch.cuda.device(device) if other else _NO_GUARD:
+        if stream is not None:
+            for t in scratch:
+                if t is not None:
+                    t.record_stream(stream)
+        rc = fn(*args, _stream(stream, device))
+    _check(name, rc)
+
+
+class _NoGuard:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != ref.device):
+            raise ValueError(f"{name} must be a CUDA tensor on {ref.device}")
+
+
+def _lens(B, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1
+                              or t.shape[0] != B or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B entries")
+
+
+def _weights_tensor(t, shape, name):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
+
+
+class Kv4Cache(NamedTuple):
+    """The planes of a 4-bit KV cache (see mea_kv4_append in ``include/mea.h``):
+    codes uint8 [B, Hkv, rows, K/2] and params [B, Hkv, rows, K/64, 2] (step and zero,
+    float16 or bfloat16) of the keys and of the values, all contiguous."""
+
+    k_codes: torch.Tensor
+    k_params: torch.Tensor
+    v_codes: torch.Tensor
+    v_params: torch.Tensor
+
+
+def mea_kv4_alloc(B: int, cache_rows: int, Hkv: int, K: int, dtype=torch.bfloat16,
+                  device="cuda") -> Kv4Cache:
+    """An uninitialised 4-bit cache for rows of `dtype` (float16 or bfloat16)."""
+    if dtype not in _DTYPE:
+        raise ValueError("dtype must be float16 or bfloat16")
+    if K not in (64, 128):
+        raise ValueError("K must be 64 or 128")
+    planes = []
+    for _ in range(2):
+        planes.append(torch.empty((B, Hkv, cache_rows, K // 2), dtype=torch.uint8, device=device))
+        planes.append(torch.empty((B, Hkv, cache_rows, K // 64, 2), dtype=dtype, device=device))
+    return Kv4Cache(*planes)
+
+
+def _kv4_dims(cache: Kv4Cache, what="cache"):
+    """(B, Hkv, rows, K, dtype) of a 4-bit cache, checked."""
+    kc, kp, vc, vp = cache
+    if kc.dim() != 4 or kc.dtype != torch.uint8:
+        raise ValueError(f"{what}: codes must be uint8 [B, Hkv, rows, K/2]")
+    B, Hkv, rows, half = kc.shape
+    K = 2 * half
+    if kp.dtype not in _DTYPE or vp.dtype != kp.dtype:
+        raise ValueError(f"{what}: params must share dtype float16 or bfloat16")
+    if vc.dtype != torch.uint8 or tuple(vc.shape) != tuple(kc.shape):
+        raise ValueError(f"{what}: k_codes and v_codes must be alike")
+    if K % 64 or any(tuple(t.shape) != (B, Hkv, rows, K // 64, 2) for t in (kp, vp)):
+        raise ValueError(f"{what}: params must be [B, Hkv, rows, K/64, 2]")
+    if not all(t.is_contiguous() for t in cache):
+        raise ValueError(f"{what}: the planes must be contiguous")
+    _same_device(kc, k_params=kp, v_codes=vc, v_params=vp)
+    return B, Hkv, rows, K, kp.dtype
+
+
+def mea_kv4_append(k_new, v_new, cache: Kv4Cache, cache_seqlens, q_seqlens=None, stream=None):
+    """Puts new rows into a 4-bit cache.  k_new/v_new [B,M,Hkv,K] (any (b, m, h) strides),
+    cache_seqlens / q_seqlens int32 CUDA [B] (rows already there, and rows of the chunk, M
+    if None): rows cache_seqlens[b] .. + q_seqlens[b] of the cache are written.  The caller
+    advances cache_seqlens.  Returns the cache."""
+    B, Hkv, rows, K, dtype = _kv4_dims(cache)
+    M = k_new.shape[1] if k_new.dim() == 4 else 0
+    if tuple(k_new.shape) != (B, M, Hkv, K) or tuple(v_new.shape) != (B, M, Hkv, K):
+        raise ValueError("k_new and v_new must be [B, M, Hkv, K]")
+    if k_new.dtype != dtype or v_new.dtype != dtype:
+        raise ValueError("k_new and v_new must have the dtype of the cache's params")
+    _same_device(cache.k_codes, k_new=k_new, v_new=v_new, cache_seqlens=cache_seqlens,
+                 q_seqlens=q_seqlens)
+    _lens(B, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    _launch("mea_kv4_append", lib.mea_kv4_append, k_new.device, stream, (),
+            (_ptr(k_new), _ptr(v_new), *map(_ptr, cache), _ptr(cache_seqlens), _ptr(q_seqlens),
+             B, M, rows, Hkv, K, _bmhk_strides(k_new, "k_new"), _bmhk_strides(v_new, "v_new"),
+             _DTYPE[dtype]))
+    return cache
+
+
+def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
+                 out_rows: int | None = None, stream=None):
+    """Rows first_rows[b] .. + rows[b] (from row 0 if None) of a 4-bit cache in 16 bits:
+    (k, v), each [B, out_rows, Hkv, K] (out_rows defaults to the cache's rows, or to that of
+    k_out); rows past rows[b] are not written."""
+    B, Hkv, cap, K, dtype = _kv4_dims(cache)
+    if out_rows is None:
+        ref = k_out if k_out is not None else v_out
+        out_rows = cap if ref is None else ref.shape[1]
+    fresh = []
+    shape = (B, int(out_rows), Hkv, K)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
+        fresh.append(k_out)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
+        fresh.append(v_out)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{name} must be {list(shape)} of the params' dtype")
+    _same_device(cache.k_codes, k_out=k_out, v_out=v_out, rows=rows, first_rows=first_rows)
+    _lens(B, rows=rows, first_rows=first_rows)
+    _launch("mea_kv4_read", lib.mea_kv4_read, k_out.device, stream, fresh,
+            (*map(_ptr, cache), _ptr(rows), _ptr(first_rows), _ptr(k_out), _ptr(v_out), B, cap,
+             shape[1], Hkv, K, _bmhk_strides(k_out, "k_out"), _bmhk_strides(v_out, "v_out"),
+             _DTYPE[dtype]))
+    return k_out, v_out
+
+
+def mea_decode_kv4_workspace_size(B: int, Hq: int, Hkv: int, K: int, max_kv_len: int,
+                                  weights: bool = False) -> int:
+    return int(lib.mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, int(bool(weights))))
+
+
+def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float | None = None,
+                   alibi: bool = False, weights=None, weights_out=None,
+                   return_weights: bool = False, out=None, lse=None, workspace=None,
+                   return_lse: bool = True, stream=None):
+    """One decode step against a 4-bit cache.  q [B,Hq,K] or [B,1,Hq,K]; kv_seqlens int32
+    CUDA [B], the rows of each sequence (its new token included) -> (out shaped like q, lse
+    [B,Hq] fp32 or None).
+
+    With ``return_weights`` (or ``weights_out``) a third result: weights_out [B,Hkv,rows]
+    fp32 = ``weights`` (zeros if None) + the softmax weight each row got in this step, summed
+    over the query heads of its kv head; 0 for rows past kv_seqlens[b].  weights_out may be
+    weights itself."""
+    B, Hkv, cap, K, dtype = _kv4_dims(cache)
+    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1) or q.shape[0] != B \
+            or q.shape[-1] != K:
+        raise ValueError("q must be [B, Hq, K] or [B, 1, Hq, K]")
+    Hq = q.shape[-2]
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if q.dtype != dtype:
+        raise ValueError("q must have the dtype of the cache's params")
+    scale = K ** -0.5 if scale is None else float(scale)
+    dev, fresh = q.device, []
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=dtype, device=dev)
+        fresh.append(out)
+    if tuple(out.shape) != tuple(q.shape) or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous and shaped and typed like q")
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        fresh.append(lse)
+    _weights_tensor(lse, (B, Hq), "lse")
+    want = return_weights or weights_out is not None
+    if weights is not None and not want:
+        raise ValueError("weights needs return_weights or weights_out")
+    if want and weights_out is None:
+        weights_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=dev)
+        fresh.append(weights_out)
+    _weights_tensor(weights, (B, Hkv, cap), "weights")
+    _weights_tensor(weights_out, (B, Hkv, cap), "weights_out")
+    _same_device(q, cache=cache.k_codes, kv_seqlens=kv_seqlens, out=out, lse=lse, weights=weights,
+                 weights_out=weights_out, workspace=workspace)
+    _lens(B, kv_seqlens=kv_seqlens)
+    need = mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, want)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        fresh.append(workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("mea_decode_kv4", lib.mea_decode_kv4, dev, stream, fresh,
+            (_ptr(q), *map(_ptr, cache), _ptr(kv_seqlens), _ptr(out), _ptr(lse), _ptr(weights),
+             _ptr(weights_out), B, Hq, Hkv, K, cap, int(max_kv_len), _DTYPE[dtype],
+             int(bool(alibi)), scale, _ptr(workspace), ws_bytes))
+    return (out, lse, weights_out) if want else (out, lse)
+
+
+def mea_key_weights(q, k, lse, cache_seqlens=None, q_seqlens=None, causal: bool = True,
+                    scale: float | None = None, alibi: bool = False, weights=None, out=None,
+                    stream=None):
+    """The attention weight every key gathered from the queries q [B,M,Hq,K], summed over
+    the rows and over the query heads of its kv head: out [B,Hkv,N] fp32 = ``weights`` (zeros
+    if None) + sum exp(scale q.k + bias - lse).  k [B,N,Hkv,K] is the keys of mea_fwd or, with
+    ``cache_seqlens`` (and ``q_seqlens``) as given to mea_prefill_chunk, the cache; lse
+    [B,Hq,M] is what that attention returned.  Rows past the sequence get 0.  out may be
+    weights itself."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, M, Hq, K] and k [B, N, Hkv, K]")
+    B, M, Hq, K = q.shape
+    N, Hkv = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (B, N, Hkv, K):
+        raise ValueError("k must be [B, N, Hkv, K]")
+    if q.dtype not in _DTYPE or k.dtype != q.dtype:
+        raise ValueError("q and k must share dtype float16 or bfloat16")
+    if q_seqlens is not None and cache_seqlens is None:
+        raise ValueError("q_seqlens needs cache_seqlens")
+    _weights_tensor(lse, (B, Hq, M), "lse")
+    scale = K ** -0.5 if scale is None else float(scale)
+    fresh = []
+    if out is None:
+        out = torch.empty((B, Hkv, N), dtype=torch.float32, device=q.device)
+        fresh.append(out)
+    _weights_tensor(weights, (B, Hkv, N), "weights")
+    _weights_tensor(out, (B, Hkv, N), "out")
+    _same_device(q, k=k, lse=lse, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens,
+                 weights=weights, out=out)
+    _lens(B, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    _launch("mea_key_weights", lib.mea_key_weights, q.device, stream, fresh,
+            (_ptr(q), _ptr(k), _ptr(lse), _ptr(cache_seqlens), _ptr(q_seqlens), _ptr(weights),
+             _ptr(out), B, M, N, Hq, Hkv, K, _bmhk_strides(q, "q"), _bmhk_strides(k, "k"),
+             _DTYPE[q.dtype], int(bool(causal)), int(bool(alibi)), scale))
+    return out
+
+
+def _planes_of(cache, what):
+    """A cache as ([(tensor, (row axis, head axis))], B, Hkv, rows): a Kv4Cache, or a
+    (k_cache, v_cache) pair of [B, rows, Hkv, K] tensors with contiguous K."""
+    if isinstance(cache, Kv4Cache):
+        B, Hkv, rows, _, _ = _kv4_dims(cache, what)
+        return [(t, (2, 1)) for t in cache], B, Hkv, rows
+    k, v = cache
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{what}: {name} must be [B, rows, Hkv, K] with contiguous K")
+        if t.dtype not in _DTYPE:
+            raise ValueError(f"{what}: {name} must be float16 or bfloat16")
+    if k.shape[:3] != v.shape[:3]:
+        raise ValueError(f"{what}: k and v must have the same rows and heads")
+    _same_device(k, v=v)
+    return [(k, (1, 2)), (v, (1, 2))], k.shape[0], k.shape[2], k.shape[1]
+
+
+def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out=None,
+                    weights_out=None, new_seqlens=None, kept=None, stream=None):
+    """Cuts each sequence of a cache down to ``budget`` rows, per kv head: the newest
+    ``recent`` and the heaviest others by ``weights`` [B,Hkv,rows] fp32 (equal weights: the
+    lowest row), moved to the front in their old order together with their weights.
+
+    cache: a Kv4Cache or a (k_cache, v_cache) pair of [B,rows,Hkv,K] tensors.  out: another
+    cache of the same kind with at least ``budget`` rows, or None to work in place (then
+    weights are cut in place too).  Returns (new_seqlens int32 [B], kept int32 [B,Hkv,budget]
+    -- the old row of every kept row, -1 after the last --, weights_out [B,Hkv,out rows], 0
+    past the kept rows)."""
+    src, B, Hkv, rows = _planes_of(cache, "cache")
+    if out is None:
+        dst, out_rows = src, rows
+        if weights_out is not None and weights_out.data_ptr() != weights.data_ptr():
+            raise ValueError("in place, weights are cut in place too")
+        weights_out = weights
+    else:
+        dst, Bo, Ho, out_rows = _planes_of(out, "out")
+        if isinstance(cache, Kv4Cache) != isinstance(out, Kv4Cache) or (Bo, Ho) != (B, Hkv):
+            raise ValueError("out must be a cache of the same kind, batch and heads")
+    budget, recent = int(budget), int(recent)
+    dev, fresh = src[0][0].device, []
+    if weights_out is None:
+        weights_out = torch.empty((B, Hkv, out_rows), dtype=torch.float32, device=dev)
+        fresh.append(weights_out)
+    if new_seqlens is None:
+        new_seqlens = torch.empty(B, dtype=torch.int32, device=dev)
+        fresh.append(new_seqlens)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
+        fresh.append(kept)
+    _weights_tensor(weights, (B, Hkv, rows), "weights")
+    _weights_tensor(weights_out, (B, Hkv, out_rows), "weights_out")
+    if kept.dtype != torch.int32 or tuple(kept.shape) != (B, Hkv, budget) \
+            or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 [B, Hkv, budget] tensor")
+    _same_device(src[0][0], weights=weights, weights_out=weights_out, kept=kept,
+                 cache_seqlens=cache_seqlens, new_seqlens=new_seqlens, out=dst[0][0])
+    _lens(B, cache_seqlens=cache_seqlens, new_seqlens=new_seqlens)
+    planes = (_Plane * len(src))()
+    for p, ((s, (r, h)), (d, _)) in enumerate(zip(src, dst)):
+        if s.dtype != d.dtype or s.shape[3:] != d.shape[3:]:
+            raise ValueError("out must have the rows of the cache")
+        size = s.element_size()
+        planes[p] = _Plane(s.data_ptr(), d.data_ptr(),
+                           _i64x3(*(s.stride(x) * size for x in (0, r, h))),
+                           _i64x3(*(d.stride(x) * size for x in (0, r, h))),
+                           s[0, 0, 0].numel() * size if s.numel() else 0)
+    _launch("mea_cache_evict", lib.mea_cache_evict, dev, stream, fresh,
+            (planes, len(src), _ptr(weights), _ptr(weights_out), _ptr(cache_seqlens),
+             _ptr(new_seqlens), _ptr(kept), B, Hkv, rows, out_rows, budget, recent))
+    return new_seqlens, kept, weights_out
 
 
 def read_device_status(clear: bool = True, stream=None) -> int:

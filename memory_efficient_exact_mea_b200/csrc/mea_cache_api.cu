@@ -1,0 +1,384 @@
+// mea_cache_api.cu -- C ABI of the cache operators declared in include/mea.h
+// (4-bit cache, gathered key weights, eviction): host-side validation, launch
+// plans and dispatch.  No allocation, no state.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mea.h"
+#include "mea_internal.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool strides_ok(const int64_t s[3]) {
+  for (int i = 0; i < 3; ++i)
+    if (s[i] <= 0 || (s[i] & 7) != 0 || s[i] >= (int64_t(1) << 38)) return false;
+  return true;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+// Splits of one decode call.  A split is a whole number of 128-row steps (four
+// warps of 32 rows); long enough that its partial state (K floats a head) and
+// its start-up stay small beside the rows it reads, short enough that the grid
+// fills the GPU's resident CTAs a few times over.
+struct DecodePlan {
+  int head_blocks, chunk, splits;
+};
+
+DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
+  DecodePlan p{};
+  p.head_blocks = (Hq / Hkv + 7) / 8;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * p.head_blocks;
+  const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
+  int64_t chunk = (max_len + want - 1) / want;
+  chunk = std::min<int64_t>(1024, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  p.chunk = static_cast<int>(chunk);
+  p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_params,
+                   void* v_codes, void* v_params, const int32_t* cache_seqlens,
+                   const int32_t* q_seqlens, int B, int M, int cache_rows, int Hkv, int K,
+                   const int64_t kn_strides[3], const int64_t vn_strides[3], mea_dtype_t dtype,
+                   cudaStream_t stream) {
+  if (B < 0 || M < 0 || cache_rows < 0 || Hkv <= 0) return MEA_ERR_INVALID_ARG;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_INVALID_ARG;
+  if (!kn_strides || !vn_strides) return MEA_ERR_INVALID_ARG;
+  if (B == 0 || M == 0) return MEA_OK;
+  if (!k_new || !v_new || !k_codes || !k_params || !v_codes || !v_params || !cache_seqlens)
+    return MEA_ERR_INVALID_ARG;
+  if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  for (const void* p : {k_new, v_new, static_cast<const void*>(k_codes),
+                        static_cast<const void*>(k_params), static_cast<const void*>(v_codes),
+                        static_cast<const void*>(v_params)})
+    if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
+  if (!strides_ok(kn_strides) || !strides_ok(vn_strides)) return MEA_ERR_UNSUPPORTED;
+  mea::Kv4AppendArgs a{};
+  a.rows = static_cast<int64_t>(B) * Hkv * M;
+  if (static_cast<int64_t>(B) * Hkv > kMaxRows / M) return MEA_ERR_UNSUPPORTED;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_codes = k_codes;
+  a.k_params = k_params;
+  a.v_codes = v_codes;
+  a.v_params = v_params;
+  a.cache_len = cache_seqlens;
+  a.q_lens = q_seqlens;
+  a.status = mea::device_status_word();
+  if (!a.status) return MEA_ERR_CUDA;
+  for (int i = 0; i < 3; ++i) {
+    a.kn_s[i] = kn_strides[i];
+    a.vn_s[i] = vn_strides[i];
+  }
+  a.M = M;
+  a.Hkv = Hkv;
+  a.cap = cache_rows;
+  return mea::launch_kv4_append(a, K, dtype == MEA_BF16, stream) == cudaSuccess ? MEA_OK
+                                                                                : MEA_ERR_CUDA;
+}
+
+int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
+                 const void* v_params, const int32_t* rows, const int32_t* first_rows,
+                 void* k_out, void* v_out, int B, int cache_rows, int out_rows, int Hkv, int K,
+                 const int64_t ko_strides[3], const int64_t vo_strides[3], mea_dtype_t dtype,
+                 cudaStream_t stream) {
+  if (B < 0 || out_rows < 0 || cache_rows < 0 || Hkv <= 0) return MEA_ERR_INVALID_ARG;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_INVALID_ARG;
+  if (!ko_strides || !vo_strides) return MEA_ERR_INVALID_ARG;
+  if (B == 0 || out_rows == 0) return MEA_OK;
+  if (!k_codes || !k_params || !v_codes || !v_params || !rows || !k_out || !v_out)
+    return MEA_ERR_INVALID_ARG;
+  if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  for (const void* p : {k_codes, k_params, v_codes, v_params, static_cast<const void*>(k_out),
+                        static_cast<const void*>(v_out)})
+    if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
+  if (!strides_ok(ko_strides) || !strides_ok(vo_strides)) return MEA_ERR_UNSUPPORTED;
+  mea::Kv4ReadArgs a{};
+  a.total = static_cast<int64_t>(B) * Hkv * out_rows;
+  if (static_cast<int64_t>(B) * Hkv > kMaxRows / out_rows) return MEA_ERR_UNSUPPORTED;
+  a.k_codes = k_codes;
+  a.k_params = k_params;
+  a.v_codes = v_codes;
+  a.v_params = v_params;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.rows = rows;
+  a.first = first_rows;
+  a.status = mea::device_status_word();
+  if (!a.status) return MEA_ERR_CUDA;
+  for (int i = 0; i < 3; ++i) {
+    a.ko_s[i] = ko_strides[i];
+    a.vo_s[i] = vo_strides[i];
+  }
+  a.out_rows = out_rows;
+  a.Hkv = Hkv;
+  a.cap = cache_rows;
+  return mea::launch_kv4_read(a, K, dtype == MEA_BF16, stream) == cudaSuccess ? MEA_OK
+                                                                              : MEA_ERR_CUDA;
+}
+
+// Workspace: partial outputs, partial log-sum-exps (both only with several
+// splits or weights), scores (weights only), each 256-byte aligned.
+static size_t kv4_workspace(int B, int Hq, int Hkv, int K, int max_len, bool weights,
+                            size_t* lse_at, size_t* score_at) {
+  const DecodePlan p = decode_plan(B, Hq, Hkv, max_len);
+  const size_t rows = static_cast<size_t>(B) * Hq;
+  size_t at = 0;
+  if (p.splits > 1) at += align256(rows * p.splits * K * sizeof(float));
+  *lse_at = at;
+  if (p.splits > 1 || weights) at += align256(rows * p.splits * sizeof(float));
+  *score_at = at;
+  if (weights) at += align256(rows * static_cast<size_t>(max_len) * sizeof(float));
+  return at;
+}
+
+size_t mea_decode_kv4_workspace_size(int B, int Hq, int Hkv, int K, int max_kv_len, int weights) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || K <= 0 || max_kv_len < 0) return 0;
+  size_t l, s;
+  return kv4_workspace(B, Hq, Hkv, K, max_kv_len, weights != 0, &l, &s);
+}
+
+int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                   const void* v_params, const int32_t* kv_seqlens, void* out, float* lse,
+                   const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int K,
+                   int cache_rows, int max_kv_len, mea_dtype_t dtype, int alibi, float scale,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || cache_rows < 0 || max_kv_len < 0)
+    return MEA_ERR_INVALID_ARG;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_INVALID_ARG;
+  if (!(scale == scale)) return MEA_ERR_INVALID_ARG;
+  if (weights_in && !weights_out) return MEA_ERR_INVALID_ARG;
+  if (B == 0) return MEA_OK;
+  if (!q || !out || !kv_seqlens) return MEA_ERR_INVALID_ARG;
+  if (cache_rows > 0 && (!k_codes || !k_params || !v_codes || !v_params))
+    return MEA_ERR_INVALID_ARG;
+  if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  for (const void* p : {q, k_codes, k_params, v_codes, v_params, static_cast<const void*>(out)})
+    if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
+  size_t lse_at, score_at;
+  const size_t need =
+      kv4_workspace(B, Hq, Hkv, K, max_kv_len, weights_out != nullptr, &lse_at, &score_at);
+  if (need > 0 && (!workspace || workspace_bytes < need ||
+                   (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return MEA_ERR_WORKSPACE;
+  mea::Kv4DecodeArgs a{};
+  const DecodePlan p = decode_plan(B, Hq, Hkv, max_kv_len);
+  if (static_cast<int64_t>(Hkv) * p.head_blocks > 65535 || B > 65535) return MEA_ERR_UNSUPPORTED;
+  a.weight_blocks =
+      weights_out ? (cache_rows + mea::kv4_weight_rows() - 1) / mea::kv4_weight_rows() : 0;
+  a.merge_blocks = static_cast<int>((static_cast<int64_t>(B) * Hq + 7) / 8);
+  if (static_cast<int64_t>(B) * Hkv * a.weight_blocks + a.merge_blocks > kMaxRows ||
+      static_cast<int64_t>(B) * Hq > kMaxRows)
+    return MEA_ERR_UNSUPPORTED;
+  a.status = mea::device_status_word();
+  if (!a.status) return MEA_ERR_CUDA;
+  a.q = q;
+  a.k_codes = k_codes;
+  a.k_params = k_params;
+  a.v_codes = v_codes;
+  a.v_params = v_params;
+  a.kv_lens = kv_seqlens;
+  a.out = out;
+  a.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.part_lse = p.splits > 1 || weights_out ? reinterpret_cast<float*>(ws + lse_at) : nullptr;
+  a.scores = weights_out ? reinterpret_cast<float*>(ws + score_at) : nullptr;
+  a.score_stride = max_kv_len;
+  a.w_in = weights_in;
+  a.w_out = weights_out;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.cap = cache_rows;
+  a.max_len = std::min(max_kv_len, cache_rows);
+  a.chunk = p.chunk;
+  a.max_splits = p.splits;
+  a.head_blocks = p.head_blocks;
+  // one split writes the result itself: the merge launch has only weights to gather
+  if (p.splits == 1) a.merge_blocks = 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return mea::launch_kv4_decode(a, K, dtype == MEA_BF16, alibi != 0, stream) == cudaSuccess
+             ? MEA_OK
+             : MEA_ERR_CUDA;
+}
+
+int mea_key_weights(const void* q, const void* k, const float* lse, const int32_t* cache_seqlens,
+                    const int32_t* q_seqlens, const float* weights_in, float* weights_out, int B,
+                    int M, int N, int Hq, int Hkv, int K, const int64_t q_strides[3],
+                    const int64_t k_strides[3], mea_dtype_t dtype, int causal, int alibi,
+                    float scale, cudaStream_t stream) {
+  if (B < 0 || M < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return MEA_ERR_INVALID_ARG;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return MEA_ERR_INVALID_ARG;
+  if (!q_strides || !k_strides) return MEA_ERR_INVALID_ARG;
+  if (!(scale == scale)) return MEA_ERR_INVALID_ARG;
+  if (q_seqlens && !cache_seqlens) return MEA_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return MEA_OK;
+  if (M < 1) return MEA_ERR_INVALID_ARG;
+  if (!q || !k || !lse || !weights_out) return MEA_ERR_INVALID_ARG;
+  if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  if (scale < 0.f) return MEA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k)) return MEA_ERR_UNSUPPORTED;
+  if (!strides_ok(q_strides) || !strides_ok(k_strides)) return MEA_ERR_UNSUPPORTED;
+  const int64_t blocks = (static_cast<int64_t>(N) + mea::kWeightKeys - 1) / mea::kWeightKeys;
+  if (static_cast<int64_t>(B) * Hkv > kMaxRows / blocks) return MEA_ERR_UNSUPPORTED;
+  mea::WeightLaunch L{};
+  mea::WeightArgs& a = L.args;
+  a.status = mea::device_status_word();
+  if (!a.status) return MEA_ERR_CUDA;
+  a.group = Hq / Hkv;
+  // Few rows: the group's heads share one 16-column tile.
+  L.narrow = M <= 16;
+  a.box_heads = 1;
+  a.box_rows = 128;
+  if (L.narrow) {
+    while (a.box_heads < a.group && a.box_heads < 16) a.box_heads *= 2;
+    a.box_rows = 16 / a.box_heads;
+    while ((1 << a.box_shift) < a.box_heads) ++a.box_shift;
+  }
+  const bool bf16 = dtype == MEA_BF16;
+  if (!mea::encode_rows(&L.tmQ, q, bf16, B, M, Hq, K, q_strides, a.box_heads, a.box_rows) ||
+      !mea::encode_rows(&L.tmK, k, bf16, B, N, Hkv, K, k_strides, 1, mea::kWeightKeys))
+    return MEA_ERR_CUDA;
+  a.lse = lse;
+  a.w_in = weights_in;
+  a.w_out = weights_out;
+  a.cache_len = cache_seqlens;
+  a.q_lens = q_seqlens;
+  a.B = B;
+  a.M = M;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  L.head_dim = K;
+  L.bf16 = bf16;
+  L.causal = causal != 0;
+  L.alibi = alibi != 0;
+  return mea::launch_weights(L, stream) == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+}
+
+// First byte past the rows an array of `rows` x Hkv x B rows touches.
+static const uint8_t* plane_end(const void* p, const int64_t st[3], int B, int rows, int Hkv,
+                                int row_bytes) {
+  return static_cast<const uint8_t*>(p) + st[0] * (B - 1) + st[1] * (rows - 1) +
+         st[2] * (Hkv - 1) + row_bytes;
+}
+
+int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weights,
+                    float* weights_out, const int32_t* cache_seqlens, int32_t* new_seqlens,
+                    int32_t* kept, int B, int Hkv, int cache_rows, int out_rows, int budget,
+                    int recent, cudaStream_t stream) {
+  if (B < 0 || Hkv <= 0 || cache_rows < 0 || out_rows < 0) return MEA_ERR_INVALID_ARG;
+  if (n_planes < 1 || n_planes > 4 || !planes) return MEA_ERR_INVALID_ARG;
+  if (budget < 1 || budget > out_rows || recent < 0 || recent > budget) return MEA_ERR_INVALID_ARG;
+  if (B == 0) return MEA_OK;
+  if (!cache_seqlens || !new_seqlens || cache_seqlens == new_seqlens || !kept || !weights_out ||
+      !weights || cache_rows < 1)
+    return MEA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * Hkv > 65535) return MEA_ERR_UNSUPPORTED;
+
+  mea_plane_t all[mea::kMaxPlanes];
+  for (int p = 0; p < n_planes; ++p) all[p] = planes[p];
+  mea_plane_t& w = all[n_planes];
+  w.src = weights;
+  w.dst = weights_out;
+  w.row_bytes = 4;
+  const int64_t rows[2] = {cache_rows, out_rows};
+  for (int side = 0; side < 2; ++side) {
+    int64_t* st = side == 0 ? w.src_strides : w.dst_strides;
+    st[0] = rows[side] * Hkv * 4;
+    st[1] = 4;
+    st[2] = rows[side] * 4;
+  }
+  const int total = n_planes + 1;
+  mea::EvictArgs a{};
+  bool in_place = false;
+  for (int p = 0; p < total; ++p) {
+    const mea_plane_t& x = all[p];
+    if (!x.src || !x.dst || x.row_bytes < 4) return MEA_ERR_INVALID_ARG;
+    int64_t bits = x.row_bytes | static_cast<int64_t>(reinterpret_cast<uintptr_t>(x.src) & 15u) |
+                   static_cast<int64_t>(reinterpret_cast<uintptr_t>(x.dst) & 15u);
+    for (int i = 0; i < 3; ++i) {
+      if (x.src_strides[i] < 0 || x.dst_strides[i] < 0) return MEA_ERR_INVALID_ARG;
+      bits |= x.src_strides[i] | x.dst_strides[i];
+    }
+    if (bits & 3) return MEA_ERR_UNSUPPORTED;
+    mea::EvictPlane& e = a.planes[p];
+    e.access = (bits & 15) == 0 ? 16 : (bits & 7) == 0 ? 8 : 4;
+    e.src = static_cast<const uint8_t*>(x.src);
+    e.dst = static_cast<uint8_t*>(x.dst);
+    e.row_bytes = x.row_bytes;
+    for (int i = 0; i < 3; ++i) {
+      e.src_s[i] = x.src_strides[i];
+      e.dst_s[i] = x.dst_strides[i];
+    }
+    if (x.src == x.dst) {
+      if (out_rows != cache_rows) return MEA_ERR_INVALID_ARG;
+      for (int i = 0; i < 3; ++i)
+        if (x.src_strides[i] != x.dst_strides[i]) return MEA_ERR_INVALID_ARG;
+      in_place = true;
+    }
+  }
+  for (int d = 0; d < total; ++d)
+    for (int s = 0; s < total; ++s) {
+      if (d == s && all[d].src == all[d].dst) continue;
+      const uint8_t* d0 = a.planes[d].dst;
+      const uint8_t* d1 = plane_end(d0, all[d].dst_strides, B, out_rows, Hkv, all[d].row_bytes);
+      const uint8_t* s0 = a.planes[s].src;
+      const uint8_t* s1 = plane_end(s0, all[s].src_strides, B, cache_rows, Hkv, all[s].row_bytes);
+      // planes of one cache may interleave (a key and a value view of one array)
+      const bool same_array = all[d].src == all[d].dst && all[s].src == all[s].dst;
+      if (!same_array && d0 < s1 && s0 < d1) return MEA_ERR_INVALID_ARG;
+    }
+
+  // Blocks: (column piece of a plane) x (sequence, kv head) x row segment.  Into
+  // other memory the rows are shared out; in place a piece's rows are one block's,
+  // so narrow pieces make the parallelism when there are few (sequence, head)s.
+  const int64_t bh = static_cast<int64_t>(B) * Hkv;
+  a.seg_rows = in_place ? budget : std::max(256, (budget + 65534) / 65535);
+  const int64_t segs = (budget + a.seg_rows - 1) / a.seg_rows;
+  int pieces = 0;
+  for (int p = 0; p < total; ++p) {
+    mea::EvictPlane& e = a.planes[p];
+    e.piece_bytes = e.row_bytes;
+    // at most 256 lanes of `access` bytes; halved further while the grid is small
+    while (e.piece_bytes % (2 * e.access) == 0 &&
+           (e.piece_bytes / e.access > 256 ||
+            (e.piece_bytes > 32 && bh * segs * n_planes * (e.row_bytes / e.piece_bytes) < 148 * 4)))
+      e.piece_bytes /= 2;
+    if (e.piece_bytes / e.access > 256) return MEA_ERR_UNSUPPORTED;
+    a.first_block[p] = pieces;
+    pieces += e.row_bytes / e.piece_bytes;
+  }
+  a.first_block[total] = pieces;
+  a.n_planes = total;
+  a.weights = weights;
+  a.w_out = weights_out;
+  a.lens = cache_seqlens;
+  a.new_lens = new_seqlens;
+  a.kept = kept;
+  a.status = mea::device_status_word();
+  if (!a.status) return MEA_ERR_CUDA;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.cap = cache_rows;
+  a.out_rows = out_rows;
+  a.budget = budget;
+  a.recent = recent;
+  return mea::launch_evict(a, stream) == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+}
+
+}  // extern "C"

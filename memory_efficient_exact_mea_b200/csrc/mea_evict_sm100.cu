@@ -1,0 +1,259 @@
+// mea_evict_sm100.cu -- eviction from a cache by gathered attention weight.
+//
+// Of a sequence's n rows a kv head keeps, when n > budget, the newest `recent`
+// and the budget - recent heaviest of the others (equal weights: the lowest row;
+// NaN: as the lightest), in their old order.  Two launches:
+//   evict_select  one block per (sequence, kv head): the weight of the last row
+//                 to keep by three counting passes over 11, 11 and 10 bits of an
+//                 order-preserving integer, then the kept row numbers by counting
+//                 in row order (ballots and a scan: no atomic decides an order);
+//   evict_move    rows kept[r] -> r of every plane.  In place a block owns a
+//                 column strip of one (sequence, head) and walks the tiles of
+//                 rows upwards: kept[r] >= r, so a tile's sources lie at or past
+//                 it, and one barrier between a tile's loads and its stores is
+//                 all the order there is to keep.  Into another cache, blocks
+//                 also share out the rows.
+#include <math.h>
+
+#include "mea_internal.h"
+#include "sm100.cuh"
+
+namespace mea {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelTile = 4 * kSelThreads;
+constexpr int kBins = 2048;
+
+// An unsigned integer ordered as the float is; NaN below everything, -0 as 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t warp_sum[32];
+  __shared__ uint32_t s_bin, s_above;
+  __shared__ uint32_t counts[128];
+  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x - b * a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = a.lens[b];
+  int32_t* kept = a.kept + static_cast<long long>(blockIdx.x) * a.budget;
+  if (n < 0 || n > a.cap) {
+    if (kvh == 0 && tid == 0) {
+      record_error(a.status, kErrInvalidArg);
+      a.new_lens[b] = 0;
+    }
+    for (int r = tid; r < a.budget; r += kSelThreads) kept[r] = -1;
+    return;
+  }
+  if (kvh == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
+  if (n <= a.budget) {
+    for (int r = tid; r < a.budget; r += kSelThreads) kept[r] = r < n ? r : -1;
+    return;
+  }
+  const float* w = a.weights + static_cast<long long>(blockIdx.x) * a.cap;
+  const int m = n - a.recent;        // candidates
+  const int take = a.budget - a.recent;  // < m
+  for (int r = tid; r < a.recent; r += kSelThreads) kept[take + r] = m + r;
+  if (take == 0) return;
+
+  uint32_t prefix = 0, need = take;  // rows still to find among those with this prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    const int above = pass == 0 ? 0 : pass == 1 ? 21 : 10;  // bits already fixed start here
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int j = tid; j < m; j += kSelThreads) {
+      const uint32_t key = order_key(w[j]);
+      if (pass == 0 || (key >> above) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1u);
+    }
+    __syncthreads();
+    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+    const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+    uint32_t sum = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    uint32_t before = lane < warp ? warp_sum[lane] : 0u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    const uint32_t excl = before + sum - c0 - c1;  // keys in higher bins
+    if (excl < need && need <= excl + c0) {
+      s_bin = kBins - 1 - 2 * tid;
+      s_above = excl;
+    } else if (excl + c0 < need && need <= excl + c0 + c1) {
+      s_bin = kBins - 2 - 2 * tid;
+      s_above = excl + c0;
+    }
+    __syncthreads();
+    prefix = pass == 0 ? s_bin : pass == 1 ? (prefix << 11) | s_bin : (prefix << 10) | s_bin;
+    need -= s_above;
+    __syncthreads();
+  }
+
+  // Rows above the key `prefix` are kept, and the first `need` equal to it.
+  uint32_t base = 0;  // rows so far: above in the low half-word counts, equal kept apart
+  uint32_t base_eq = 0;
+#pragma unroll 1
+  for (int t0 = 0; t0 < m; t0 += kSelTile) {
+    uint32_t gt[4], eq[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = t0 + u * kSelThreads + tid;
+      const uint32_t key = j < m ? order_key(w[j]) : 0u;
+      gt[u] = __ballot_sync(0xffffffffu, j < m && key > prefix);
+      eq[u] = __ballot_sync(0xffffffffu, j < m && key == prefix);
+      if (lane == 0) counts[u * 32 + warp] = __popc(gt[u]) | (__popc(eq[u]) << 16);
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive scan of the 128 counts (at most 4096 each: no carry)
+      uint32_t v[4], run = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = run;
+        run += counts[lane * 4 + i];
+      }
+      uint32_t incl = run;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) counts[lane * 4 + i] = v[i] + incl - run;
+      if (lane == 31) warp_sum[0] = incl;
+    }
+    __syncthreads();
+    const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t c = counts[u * 32 + warp];
+      const uint32_t ngt = base + (c & 0xffffu) + __popc(gt[u] & lower);
+      const uint32_t neq = base_eq + (c >> 16) + __popc(eq[u] & lower);
+      const bool is_eq = (eq[u] >> lane) & 1u;
+      if (((gt[u] >> lane) & 1u) || (is_eq && neq < need))
+        kept[ngt + min(neq, need)] = t0 + u * kSelThreads + tid;
+    }
+    base += warp_sum[0] & 0xffffu;
+    base_eq += warp_sum[0] >> 16;
+    __syncthreads();
+  }
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 8;
+
+template <int A>
+struct Word;
+template <>
+struct Word<16> { uint32_t v[4]; };
+template <>
+struct Word<8> { uint32_t v[2]; };
+template <>
+struct Word<4> { uint32_t v[1]; };
+
+// Plain (not read-only-cache) accesses: the planes may be rewritten in place.
+template <int A>
+__device__ __forceinline__ Word<A> load_word(const uint8_t* p) {
+  Word<A> w;
+  if constexpr (A == 16)
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.v[0]), "=r"(w.v[1]), "=r"(w.v[2]), "=r"(w.v[3]) : "l"(p) : "memory");
+  else if constexpr (A == 8)
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(w.v[0]), "=r"(w.v[1]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(w.v[0]) : "l"(p) : "memory");
+  return w;
+}
+
+template <int A>
+__device__ __forceinline__ void store_word(uint8_t* p, const Word<A>& w) {
+  if constexpr (A == 16)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w.v[0], w.v[1], w.v[2], w.v[3]);
+  else if constexpr (A == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(w.v[0], w.v[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = w.v[0];
+}
+
+template <int A>
+__device__ void move_rows(const EvictPlane& pl, const uint8_t* src, uint8_t* dst,
+                          const int32_t* kept, int r_begin, int r_end) {
+  const int lanes = pl.piece_bytes / A;
+  const int part = threadIdx.x % lanes, sub = threadIdx.x / lanes;
+  const int per = kMoveThreads / lanes;  // rows per unroll step
+  const int tile = per * kMoveUnroll;
+  const bool mine = sub < per;
+  Word<A> cur[kMoveUnroll], nxt[kMoveUnroll];
+  auto fetch = [&](Word<A>(&w)[kMoveUnroll], int r0) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int r = r0 + u * per + sub;
+      if (mine && r < r_end)
+        w[u] = load_word<A>(src + kept[r] * pl.src_s[1] + part * A);
+    }
+  };
+  fetch(cur, r_begin);
+  for (int r0 = r_begin; r0 < r_end; r0 += tile) {
+    fetch(nxt, r0 + tile);  // sources from row r0 + tile on: this tile's stores end there
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int r = r0 + u * per + sub;
+      if (mine && r < r_end) store_word<A>(dst + r * pl.dst_s[1] + part * A, cur[u]);
+      cur[u] = nxt[u];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  int p = 0;
+  while (p + 1 < a.n_planes && static_cast<int>(blockIdx.x) >= a.first_block[p + 1]) ++p;
+  const EvictPlane& pl = a.planes[p];
+  const int piece = blockIdx.x - a.first_block[p];
+  const int bh = blockIdx.y, b = bh / a.Hkv, kvh = bh - b * a.Hkv;
+  const int n = a.lens[b];
+  if (n < 0 || n > a.cap) return;  // evict_select has recorded it
+  const int count = min(n, a.budget);
+  const int r_begin = blockIdx.z * a.seg_rows;
+  const int r_end = min(count, r_begin + a.seg_rows);
+  const uint8_t* src = pl.src + b * pl.src_s[0] + kvh * pl.src_s[2] + piece * pl.piece_bytes;
+  uint8_t* dst = pl.dst + b * pl.dst_s[0] + kvh * pl.dst_s[2] + piece * pl.piece_bytes;
+  // in place, a sequence within its budget stays where it is
+  if (r_begin < r_end && !(pl.src == pl.dst && n <= a.budget)) {
+    const int32_t* kept = a.kept + static_cast<long long>(bh) * a.budget;
+    if (pl.access == 16) move_rows<16>(pl, src, dst, kept, r_begin, r_end);
+    else if (pl.access == 8) move_rows<8>(pl, src, dst, kept, r_begin, r_end);
+    else move_rows<4>(pl, src, dst, kept, r_begin, r_end);
+  }
+  if (pl.dst == reinterpret_cast<uint8_t*>(a.w_out) && blockIdx.z == 0) {
+    __syncthreads();  // in place: after the weights have moved down
+    float* w = a.w_out + static_cast<long long>(bh) * a.out_rows;
+    for (int r = count + threadIdx.x; r < a.out_rows; r += kMoveThreads) w[r] = 0.f;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
+  evict_select_kernel<<<a.B * a.Hkv, kSelThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(a.first_block[a.n_planes], a.B * a.Hkv,
+                  (a.budget + a.seg_rows - 1) / a.seg_rows);
+  evict_move_kernel<<<grid, kMoveThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mea
