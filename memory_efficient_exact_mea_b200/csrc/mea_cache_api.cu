@@ -22,6 +22,18 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
+// Up to 8 rows of a head at a time; false if the batch has 2^31 rows or more.
+bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
+  o->shift = M >= 8 ? 3 : M >= 4 ? 2 : M >= 2 ? 1 : 0;
+  const int64_t tiles = (static_cast<int64_t>(M) + (1 << o->shift) - 1) >> o->shift;
+  const int64_t per = tiles << o->shift;
+  if (static_cast<int64_t>(B) * Hkv > kMaxRows / per) return false;
+  o->total = static_cast<uint32_t>(per * B * Hkv);
+  o->heads = mea::fast_div(static_cast<uint32_t>(Hkv));
+  o->tiles = mea::fast_div(static_cast<uint32_t>(tiles));
+  return true;
+}
+
 // Splits of one decode call.  A split is a whole number of 128-row steps (four
 // warps of 32 rows); long enough that its partial state (K floats a head) and
 // its start-up stay small beside the rows it reads, short enough that the grid
@@ -64,8 +76,7 @@ int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_
     if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
   if (!strides_ok(kn_strides) || !strides_ok(vn_strides)) return MEA_ERR_UNSUPPORTED;
   mea::Kv4AppendArgs a{};
-  a.rows = static_cast<int64_t>(B) * Hkv * M;
-  if (static_cast<int64_t>(B) * Hkv > kMaxRows / M) return MEA_ERR_UNSUPPORTED;
+  if (!row_order(&a.order, B, M, Hkv)) return MEA_ERR_UNSUPPORTED;
   a.k_new = k_new;
   a.v_new = v_new;
   a.k_codes = k_codes;
@@ -104,8 +115,7 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
     if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
   if (!strides_ok(ko_strides) || !strides_ok(vo_strides)) return MEA_ERR_UNSUPPORTED;
   mea::Kv4ReadArgs a{};
-  a.total = static_cast<int64_t>(B) * Hkv * out_rows;
-  if (static_cast<int64_t>(B) * Hkv > kMaxRows / out_rows) return MEA_ERR_UNSUPPORTED;
+  if (!row_order(&a.order, B, out_rows, Hkv)) return MEA_ERR_UNSUPPORTED;
   a.k_codes = k_codes;
   a.k_params = k_params;
   a.v_codes = v_codes;

@@ -150,6 +150,23 @@ bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int batch, int r
 // ---------------------------------------------------------------------------
 // 4-bit cache (mea_kv4_sm100.cu): planes [B, Hkv, cap, ...], contiguous.
 // ---------------------------------------------------------------------------
+// x / d for x < 2^31: (hi32(x m) + x) >> s.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while ((uint64_t(1) << f.s) < d) ++f.s;
+  f.m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.s) - d)) / d + 1);
+  return f;
+}
+
+// Flat order of (sequence, row, head): 2^shift rows of a head, next head, next rows.
+struct RowOrder {
+  FastDiv heads, tiles;
+  uint32_t shift, total;  // total < 2^31
+};
+
 struct Kv4AppendArgs {
   const void *k_new, *v_new;
   void *k_codes, *k_params, *v_codes, *v_params;
@@ -157,7 +174,7 @@ struct Kv4AppendArgs {
   const int32_t* q_lens;  // nullptr: M
   int* status;
   long long kn_s[3], vn_s[3];
-  long long rows;  // B * Hkv * M
+  RowOrder order;
   int M, Hkv, cap;
 };
 
@@ -168,7 +185,7 @@ struct Kv4ReadArgs {
   const int32_t* first;  // [B] or nullptr: 0
   int* status;
   long long ko_s[3], vo_s[3];
-  long long total;  // B * Hkv * out_rows
+  RowOrder order;
   int out_rows, Hkv, cap;
 };
 

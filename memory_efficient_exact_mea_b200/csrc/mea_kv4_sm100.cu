@@ -36,25 +36,58 @@ __device__ __forceinline__ uint32_t to_16(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Store.  Eight lanes hold one group of 64 (16 bytes each); minimum and maximum
-// by shuffles.  Consecutive lanes walk rows of one head, so the 16-bit rows are
-// read in segments of K * 2 bytes and the codes are written contiguously.
-// Bound by memory: 4.6 bytes per element pair against ~12 instructions.
+// Rows of a [B, M, Hkv] batch in one flat order: a few rows (2^shift) of one head,
+// then the next head, then the next rows.  A block's share is then one contiguous
+// piece of the 16-bit side ([B, M, Hkv, K]) and runs of a few whole rows on the
+// 4-bit side ([B, Hkv, rows, ...]), whatever M is.  (Head by head, 2 KB apart on the
+// 16-bit side, the same kernels took 1.5 to 2 times as long.)
 // ---------------------------------------------------------------------------
+struct RowAt {
+  unsigned b, h, r;
+};
+__device__ __forceinline__ unsigned divide(unsigned x, const FastDiv& d) {
+  return (__umulhi(x, d.m) + x) >> d.s;
+}
+__device__ __forceinline__ RowAt row_at(unsigned i, const RowOrder& o) {
+  RowAt x;
+  const unsigned q = i >> o.shift;
+  const unsigned q2 = divide(q, o.heads);
+  x.h = q - q2 * o.heads.d;
+  x.b = divide(q2, o.tiles);
+  x.r = ((q2 - x.b * o.tiles.d) << o.shift) + (i & ((1u << o.shift) - 1u));
+  return x;
+}
+
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;
 
-// The nearest integer to (x - z) / s, ties to even, decided exactly: the fp32
-// quotient is right unless it lies next to a half, and there x is compared with
-// z + s (k + 1/2), which a double holds exactly for 16-bit z and s.
-__device__ __noinline__ float code_exact(float x, float z, float s) {
-  const double q = (static_cast<double>(x) - z) / s;
-  const double k = floor(q);
-  const double edge = static_cast<double>(z) + static_cast<double>(s) * (k + 0.5);
-  const double xd = x;
-  if (fabs(q - k - 0.5) < 1e-6)
-    return static_cast<float>(xd > edge ? k + 1.0 : xd < edge ? k : rint(k + 0.5));
-  return static_cast<float>(rint(q));
+// ---------------------------------------------------------------------------
+// Store.  Eight lanes hold one group of 64 (16 bytes each); minimum and maximum
+// by shuffles.  Consecutive lanes walk rows of one head, so the 16-bit rows are
+// read in segments of K * 2 bytes and the codes are written contiguously.
+// ---------------------------------------------------------------------------
+// c = nearest integer to (x - z) / s, ties to even, decided exactly.  Adding 1.5 2^23
+// to d / s (in one fused step, d = x - z) rounds it to an integer in the low mantissa
+// bits; that is right unless the quotient lies next to a half.  There the sign of
+// x - (z + s (k + 1/2)) decides: s (k + 1/2) has at most 16 bits, d lies within a
+// factor of two of it, and the part of x - z that d lost is known, so the sign is
+// exact in fp32.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+
+__device__ __forceinline__ float code_near_half(float x, float z, float s, float inv) {
+  const float d = x - z;
+  const float bb = d - x;
+  const float lost = (x - (d - bb)) + (-z - bb);  // x - z = d + lost
+  const float q = d * inv;
+  const float k = floorf(q);
+  if (fabsf(q - k - 0.5f) > 1e-3f) return rintf(q);
+  const float over = (d - s * (k + 0.5f)) + lost;
+  return over > 0.f ? k + 1.f : over < 0.f ? k : rintf(k + 0.5f);
+}
+
+// Steps outside [2^-100, 2^100]: the same in doubles.
+__device__ __noinline__ float code_wide(float x, float z, float s) {
+  return static_cast<float>(rint((static_cast<double>(x) - z) / s));
 }
 
 template <int D, bool BF16>
@@ -64,30 +97,28 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   const int part = threadIdx.x % kLanes;
   const bool value = blockIdx.y != 0;
   const uint16_t* src = static_cast<const uint16_t*>(value ? a.v_new : a.k_new);
-  const long long* st = value ? a.vn_s : a.kn_s;
+  const long long sb = value ? a.vn_s[0] : a.kn_s[0], sr = value ? a.vn_s[1] : a.kn_s[1],
+                  sh = value ? a.vn_s[2] : a.kn_s[2];
   uint32_t* codes = static_cast<uint32_t*>(value ? a.v_codes : a.k_codes);
   uint32_t* params = static_cast<uint32_t*>(value ? a.v_params : a.k_params);
+  const unsigned first = blockIdx.x * (kRowUnroll * kRows);
 
   uint4 raw[kRowUnroll];
   long long dst[kRowUnroll];  // row of the [B, Hkv, cap] planes, or -1
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u) {
-    const long long idx = (static_cast<long long>(blockIdx.x) * kRowUnroll + u) * kRows +
-                          threadIdx.x / kLanes;
+    const unsigned off = u * kRows + threadIdx.x / kLanes;
     dst[u] = -1;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (idx < a.rows) {
-      const unsigned i = static_cast<unsigned>(idx);
-      const unsigned bh = i / static_cast<unsigned>(a.M), r = i - bh * a.M;
-      const unsigned b = bh / static_cast<unsigned>(a.Hkv), h = bh - b * a.Hkv;
-      const int n = a.q_lens ? a.q_lens[b] : a.M;
-      const int past = a.cache_len[b];
+    if (first + off < a.order.total) {
+      const RowAt x = row_at(first + off, a.order);
+      const int n = a.q_lens ? a.q_lens[x.b] : a.M;
+      const int past = a.cache_len[x.b];
       if (n < 0 || n > a.M || past < 0 || past > a.cap - n) {
-        if (r == 0 && h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
-      } else if (static_cast<int>(r) < n) {
-        dst[u] = static_cast<long long>(bh) * a.cap + past + r;
-        raw[u] = *reinterpret_cast<const uint4*>(src + b * st[0] + r * st[1] + h * st[2] +
-                                                 part * 8);
+        if (x.r == 0 && x.h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
+      } else if (static_cast<int>(x.r) < n) {
+        dst[u] = (static_cast<long long>(x.b) * a.Hkv + x.h) * a.cap + past + x.r;
+        raw[u] = *reinterpret_cast<const uint4*>(src + x.b * sb + x.r * sr + x.h * sh + part * 8);
       }
     }
   }
@@ -97,8 +128,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = to_f<BF16>(w[i] & 0xffffu);
-      x[2 * i + 1] = to_f<BF16>(w[i] >> 16);
+      x[2 * i] = BF16 ? __uint_as_float(w[i] << 16) : to_f<BF16>(w[i] & 0xffffu);
+      x[2 * i + 1] = BF16 ? __uint_as_float(w[i] & 0xffff0000u) : to_f<BF16>(w[i] >> 16);
     }
     float mn = x[0], mx = x[0], bad = 0.f;
 #pragma unroll
@@ -111,33 +142,39 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     for (int o = 1; o < 8; o <<= 1) {
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      bad += __shfl_xor_sync(0xffffffffu, bad, o);
     }
+    const unsigned bad_lanes = __ballot_sync(0xffffffffu, bad != bad);
+    const bool bad_group = ((bad_lanes >> (threadIdx.x & 24)) & 0xffu) != 0;
     const float range = mx - mn;  // may pass fp32's largest value for bf16 inputs
     const float s_raw = isinf(range) ? (0.5f * mx - 0.5f * mn) / 15.f * 2.f : range / 15.f;
     uint32_t s16 = to_16<BF16>(s_raw), z16 = to_16<BF16>(mn);
     const float s = to_f<BF16>(s16), z = mn;
     uint32_t word = 0;
-    if (bad != bad) {
+    if (bad_group) {
       s16 = z16 = BF16 ? 0x7fc0u : 0x7e00u;  // a group with a NaN or infinity stands for NaN
-    } else if (s > 0.f) {
-      float c[8], worst = 0.f;
-      // outside this range 1/s or x - z could leave fp32's range
-      const bool plain = s >= 0x1p-100f && s <= 0x1p100f;
-      const float inv = plain ? 1.f / s : 0.f;
+    } else if (s >= 0x1p-100f && s <= 0x1p100f) {
+      const float inv = 1.f / s;
+      float worst = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = (x[i] - z) * inv;
-        c[i] = rintf(t);
-        worst = fmaxf(worst, fabsf(t - c[i]));
+        const float d = x[i] - z;
+        const float m = fminf(fmaf(d, inv, kRound), kRound + 15.f);
+        worst = fmaxf(worst, fabsf(fmaf(d, inv, kRound - m)));
+        // the mantissa's low bits are the code; kRound's own bits come off below
+        word += __float_as_uint(m) << (4 * i);
       }
-      if (!plain || worst > 0.4999f) {
+      constexpr uint32_t kBits = 0x4B400000u;
+      word -= kBits + (kBits << 4) + (kBits << 8) + (kBits << 12) + (kBits << 16) +
+              (kBits << 20) + (kBits << 24) + (kBits << 28);
+      if (worst > 0.4999f) {  // a quotient next to a half (or past 15)
+        word = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = code_exact(x[i], z, s);
+        for (int i = 0; i < 8; ++i)
+          word |= static_cast<uint32_t>(fminf(code_near_half(x[i], z, s, inv), 15.f)) << (4 * i);
       }
-#pragma unroll
+    } else if (s > 0.f) {
       for (int i = 0; i < 8; ++i)
-        word |= static_cast<uint32_t>(fminf(fmaxf(c[i], 0.f), 15.f)) << (4 * i);
+        word |= static_cast<uint32_t>(fminf(fmaxf(code_wide(x[i], z, s), 0.f), 15.f)) << (4 * i);
     }
     if (dst[u] >= 0) {
       codes[dst[u] * kLanes + part] = word;
@@ -149,6 +186,17 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
 // ---------------------------------------------------------------------------
 // Load: rows [first_b, first_b + count_b) of every head back into 16 bits.
 // ---------------------------------------------------------------------------
+// c s + z in fp32 with c and s 16-bit (exact product, one rounding).
+template <bool BF16>
+__device__ __forceinline__ float fma_16(uint16_t c, uint16_t s, float z) {
+  float d;
+  if constexpr (BF16)
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(c), "h"(s), "f"(z));
+  else
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(c), "h"(s), "f"(z));
+  return d;
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs a) {
   constexpr int kLanes = D / 8;
@@ -158,42 +206,58 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
   const uint32_t* codes = static_cast<const uint32_t*>(value ? a.v_codes : a.k_codes);
   const uint32_t* params = static_cast<const uint32_t*>(value ? a.v_params : a.k_params);
   uint16_t* out = static_cast<uint16_t*>(value ? a.v_out : a.k_out);
-  const long long* st = value ? a.vo_s : a.ko_s;
+  const long long sb = value ? a.vo_s[0] : a.ko_s[0], sr = value ? a.vo_s[1] : a.ko_s[1],
+                  sh = value ? a.vo_s[2] : a.ko_s[2];
+  const unsigned first = blockIdx.x * (kRowUnroll * kRows);
 
   uint32_t word[kRowUnroll], sz[kRowUnroll];
   long long dst[kRowUnroll];
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u) {
-    const long long idx = (static_cast<long long>(blockIdx.x) * kRowUnroll + u) * kRows +
-                          threadIdx.x / kLanes;
+    const unsigned off = u * kRows + threadIdx.x / kLanes;
     dst[u] = -1;
     word[u] = sz[u] = 0;
-    if (idx < a.total) {
-      const unsigned i = static_cast<unsigned>(idx);
-      const unsigned bh = i / static_cast<unsigned>(a.out_rows), r = i - bh * a.out_rows;
-      const unsigned b = bh / static_cast<unsigned>(a.Hkv), h = bh - b * a.Hkv;
-      const int n = a.rows[b];
-      const int first = a.first ? a.first[b] : 0;
-      if (n < 0 || n > a.out_rows || first < 0 || first > a.cap - n) {
-        if (r == 0 && h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
-      } else if (static_cast<int>(r) < n) {
-        const long long row = static_cast<long long>(bh) * a.cap + first + r;
+    if (first + off < a.order.total) {
+      const RowAt x = row_at(first + off, a.order);
+      const int n = a.rows[x.b];
+      const int skip = a.first ? a.first[x.b] : 0;
+      if (n < 0 || n > a.out_rows || skip < 0 || skip > a.cap - n) {
+        if (x.r == 0 && x.h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
+      } else if (static_cast<int>(x.r) < n) {
+        const long long row = (static_cast<long long>(x.b) * a.Hkv + x.h) * a.cap + skip + x.r;
         word[u] = codes[row * kLanes + part];
         sz[u] = params[row * (D / 64) + part / 8];
-        dst[u] = b * st[0] + r * st[1] + h * st[2] + part * 8;
+        dst[u] = x.b * sb + x.r * sr + x.h * sh + part * 8;
       }
     }
   }
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u) {
-    const float s = to_f<BF16>(sz[u] & 0xffffu), z = to_f<BF16>(sz[u] >> 16);
-    uint32_t o[4];
+    const uint16_t s = static_cast<uint16_t>(sz[u]);
+    const float z = BF16 ? __uint_as_float(sz[u] & 0xffff0000u) : to_f<BF16>(sz[u] >> 16);
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = pack2<BF16>(fmaf(static_cast<float>((word[u] >> (8 * i)) & 15u), s, z),
-                         fmaf(static_cast<float>((word[u] >> (8 * i + 4)) & 15u), s, z));
+    for (int i = 0; i < 4; ++i) {  // nibbles i and i + 4 as a pair of numbers 16 + c, then c
+      uint32_t c;
+      if constexpr (BF16) {
+        const uint32_t y = i == 0 ? word[u] << 3 : word[u] >> (4 * i - 3);
+        const uint32_t m = (y & 0x00780078u) | 0x41804180u;
+        const __nv_bfloat162 k = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                         __float2bfloat162_rn(16.f));
+        c = *reinterpret_cast<const uint32_t*>(&k);
+      } else {
+        const uint32_t y = i < 2 ? word[u] << (6 - 4 * i) : word[u] >> (4 * i - 6);
+        const uint32_t m = (y & 0x03C003C0u) | 0x4C004C00u;
+        const __half2 k = __hsub2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(16.f));
+        c = *reinterpret_cast<const uint32_t*>(&k);
+      }
+      v[i] = fma_16<BF16>(static_cast<uint16_t>(c), s, z);
+      v[i + 4] = fma_16<BF16>(static_cast<uint16_t>(c >> 16), s, z);
+    }
     if (dst[u] >= 0)
-      *reinterpret_cast<uint4*>(out + dst[u]) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(out + dst[u]) =
+          make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]),
+                     pack2<BF16>(v[6], v[7]));
   }
 }
 
@@ -201,78 +265,141 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // Decode.  With the group's sums kept apart,
 //   q.k^_j = sum_g s_jg (sum_{d in g} q_d c_jd) + z_jg (sum_{d in g} q_d)
 //   out_d  = sum_j (p_j s_jg) c_jd + sum_j p_j z_jg          (d in group g)
-// so the codes go into the tensor cores as they are: a 16-bit number 16 + c is
-// made from a nibble by one shift and one and-or (its mantissa field), exact in
-// fp16 and bf16, and 16 times the other operand's sum is taken off again in
-// fp32.  No dequantised value is ever rounded; p s goes in as bf16 hi + lo.
+// so the codes go into the tensor cores as they are, and no dequantised value is
+// ever formed.  A nibble in mantissa bits [b, b + 4) of an fp16 number of exponent
+// 10 - b makes that number 2^(10 - b) + c exactly: two shifts and four and-ors turn
+// a word into four operand pairs, with offsets 256 (b = 2) and 16 (b = 6).  The
+// offsets are taken off again exactly: Q.K^T starts its accumulator at minus their
+// share, and P.V has one more accumulator whose A operand is all ones, the sum of
+// the very P values that were multiplied.
 //
-// A warp takes 32 rows at a time straight from global memory into the fragment
-// layout of mma.sync m16n8k16 (rows x heads and dimensions x heads, heads
-// padded to 8): a thread's nibbles for one row are whole words of the row, and
-// since the order of the contraction index is free, the pairs (i, i + 4) of a
-// word serve as the operand's pairs.  V pairs two rows: one byte permute joins
-// the halves of the two rows' words.  The next 32 rows are fetched while the
-// current ones are computed.  The running maximum is raised only when a score
-// passes it by 2^8, so the accumulators are rarely rescaled.
+// Both products run in fp16 whatever the input type.  q is scaled by a power of two
+// to a largest magnitude in [128, 256], exact but for values 2^-22 of that and less.
+// P' = p s is rounded to fp16 (11 bits, finer than a bf16 result's 8; mea_decode
+// rounds p the same way for fp16): the reference R of p = 2^(y - R) is chosen per
+// head so that the largest p s is about one, not the largest p, and is raised only
+// when some p s passes 2^14 (so the accumulators are rarely rescaled).
+//
+// A warp takes 32 rows at a time in the fragment layout of mma.sync m16n8k16 (rows x heads and dimensions x heads, heads padded to
+// 8): a thread's nibbles for one row are whole words of the row, and since the order
+// of the contraction index is free, the pairs (i, i + 4) of a word serve as the
+// operand's pairs.  V pairs two rows: one byte permute joins the halves of the two
+// rows' words.  Each warp copies its own tiles into a ring of its own (cp.async,
+// 16-byte chunks, no barrier but __syncwarp), two tiles ahead.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;        // rows per warp and iteration
 constexpr int kHeads = 8;        // query heads per CTA (MMA n)
-constexpr float kLazy = 8.f;     // log2 units a score may pass the running maximum
+constexpr float kNoRef = -3.0e38f;     // reference of a warp that has seen no score
+constexpr float kMaxWeight = 16384.f;  // largest p s before the reference is raised
+constexpr float kMaxPlain = 0x1p64f;   // the same for p alone (rows whose s is small)
 
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ void mma_f16_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
+}
+
+// One product of the input type, A rows (gid, gid + 8) with k = 2 tig, 2 tig + 1 only.
 template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (BF16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  }
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5}, {%6}, {%7, %7, %7, %7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5}, {%6}, {%7, %7, %7, %7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-// Nibbles N and N + 4 of w as a pair of 16-bit numbers 16 + c: bf16 has the
-// unit at mantissa bit 3 of [16, 32), fp16 at bit 6.
-template <bool BF16, int N>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  constexpr int kUp = (BF16 ? 3 : 6) - 4 * N;
-  const uint32_t x = kUp >= 0 ? w << (kUp >= 0 ? kUp : 0) : w >> (kUp < 0 ? -kUp : 0);
-  return BF16 ? ((x & 0x00780078u) | 0x41804180u) : ((x & 0x03C003C0u) | 0x4C004C00u);
+// Nibbles N and N + 4 of a word as fp16 pairs: offset 256 for even N, 16 for odd.
+struct CodePairs {
+  uint32_t n[4];
+};
+__device__ __forceinline__ CodePairs code_pairs(uint32_t w) {
+  const uint32_t lo = w << 2, hi = w >> 6;
+  return {{(lo & 0x003C003Cu) | 0x5C005C00u, (lo & 0x03C003C0u) | 0x4C004C00u,
+           (hi & 0x003C003Cu) | 0x5C005C00u, (hi & 0x03C003C0u) | 0x4C004C00u}};
+}
+constexpr float kOffEven = 256.f, kOffOdd = 16.f;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
 }
 
 template <int BYTES>
-__device__ __forceinline__ void load_words(const void* p, uint32_t* r) {
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* r) {
   if constexpr (BYTES == 8)
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
   else
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
 }
+
+template <bool BF16>
+__device__ __forceinline__ float step_of(uint32_t w) {  // low 16 bits
+  if constexpr (BF16) return __uint_as_float(w << 16);
+  else return __low2float(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float zero_of(uint32_t w) {  // high 16 bits
+  if constexpr (BF16) return __uint_as_float(w & 0xffff0000u);
+  else return __high2float(*reinterpret_cast<const __half2*>(&w));
+}
+
+constexpr int kStages = 3;  // ring of one warp: two tiles in flight, one in use
 
 template <int D>
 struct KSmem {
-  float m[kWarps][kHeads];
-  float l[kWarps][kHeads];
-  float acc[kWarps][kHeads][D];
+  static constexpr int NG = D / 64;
+  static constexpr int kCodes = kTile * D / 2;       // one plane's codes of a tile
+  static constexpr int kParams = kTile * 4 * NG;
+  static constexpr int kStage = 2 * (kCodes + kParams);  // K codes, V codes, K params, V params
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kBytes = kWarps * kWarp;
+  // after the ring: m, l [kWarps][kHeads], acc [kWarps][kHeads][D]
+  static_assert(kWarps * kHeads * (D + 2) * 4 <= kBytes, "combine area");
 };
 
+// Where 16-byte chunk c of row r of a tile lies: 128-byte lines, the chunk's slot
+// in the line turned by the line number, so that both the K reads (4 or 8 rows x
+// 32 bytes) and the V reads (every other row) touch every bank once.
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  if constexpr (D == 128)
+    return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4);
+  else
+    return (r >> 2) * 128 + (((((r & 3) << 1) | c) ^ (((r >> 2) & 1) << 1)) << 4);
+}
+
 template <int D, bool BF16, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4DecodeArgs a) {
-  constexpr int NG = D / 64;  // groups of a row
-  __shared__ KSmem<D> sm;
+__global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4DecodeArgs a) {
+  using L = KSmem<D>;
+  constexpr int NG = L::NG;  // groups of a row
+  extern __shared__ __align__(128) uint8_t smem[];
   const int split = blockIdx.x, b = blockIdx.z;
   const int kvh = blockIdx.y / a.head_blocks;
   const int g0 = (blockIdx.y - kvh * a.head_blocks) * kHeads;  // first head within the group
@@ -301,65 +428,121 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
   const long long plane = (static_cast<long long>(b) * a.Hkv + kvh) * a.cap;
   const uint8_t* kc = static_cast<const uint8_t*>(a.k_codes) + plane * (D / 2);
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_codes) + plane * (D / 2);
-  const uint32_t* kp = static_cast<const uint32_t*>(a.k_params) + plane * NG;
-  const uint32_t* vp = static_cast<const uint32_t*>(a.v_params) + plane * NG;
+  const uint8_t* kp = static_cast<const uint8_t*>(a.k_params) + plane * (4 * NG);
+  const uint8_t* vp = static_cast<const uint8_t*>(a.v_params) + plane * (4 * NG);
+  const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
 
-  uint32_t kw[4][NG][2], kq[4][NG];  // rows gid + 8 i: 16 codes a group; (s, z)
-  uint32_t vw[8][NG], vq[4][NG];     // rows 16 (i / 4) + 2 tig + (0, 1, 8, 9)[i % 4]: 8 codes a group
-  auto load_k = [&](int t) {
+  // One tile into stage `slot`; in the last tile, rows past the end take the last
+  // row again (their weight is zero).
+  constexpr int kPer = D / 32;  // 16-byte chunks of a row's codes; 8 or 16 rows a copy
+  const int chunk0 = chunk_at<D>(lane / kPer, lane % kPer);
+  auto fetch = [&](int tile, int slot) {
+    const uint32_t st = ring + slot * L::kStage, to = st + chunk0;
+    const uint32_t top = st + 2 * L::kCodes + lane * 4 * NG;
+    if (tile + kTile <= s1) {
+      const long long off = static_cast<long long>(tile) * (D / 2) + lane * 16;
+      const long long poff = static_cast<long long>(tile + lane) * (4 * NG);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long row = min(t + gid + 8 * i, s1 - 1);
+      for (int j = 0; j < kPer; ++j) {
+        copy_async<16>(to + 512 * j, kc + off + 512 * j);
+        copy_async<16>(to + 512 * j + L::kCodes, vc + off + 512 * j);
+      }
+      copy_async<4 * NG>(top, kp + poff);
+      copy_async<4 * NG>(top + L::kParams, vp + poff);
+    } else if (tile < s1) {
+      const int left = s1 - 1 - tile;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        load_words<8>(kc + row * (D / 2) + 32 * g + 8 * tig, kw[i][g]);
-      load_words<4 * NG>(kp + row * NG, kq[i]);
+      for (int j = 0; j < kPer; ++j) {
+        const int r = min(lane / kPer + 32 / kPer * j, left);
+        const long long off = static_cast<long long>(tile + r) * (D / 2) + lane % kPer * 16;
+        copy_async<16>(to + 512 * j, kc + off);
+        copy_async<16>(to + 512 * j + L::kCodes, vc + off);
+      }
+      const long long poff = static_cast<long long>(tile + min(lane, left)) * (4 * NG);
+      copy_async<4 * NG>(top, kp + poff);
+      copy_async<4 * NG>(top + L::kParams, vp + poff);
     }
-  };
-  auto load_v = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long row =
-          min(t + 16 * (i / 4) + 2 * tig + (i & 1) + 8 * ((i >> 1) & 1), s1 - 1);
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        load_words<4>(vc + row * (D / 2) + 32 * g + 4 * gid, &vw[i][g]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_words<4 * NG>(vp + static_cast<long long>(min(t + gid + 8 * i, s1 - 1)) * NG, vq[i]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int t = s0 + warp * kTile;
-  if (t < s1) {
-    load_k(t);
-    load_v(t);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(t + i * kWarps * kTile, i);
+
+  // This thread's words within a stage: K rows gid + 8 i, 8 bytes at 8 tig of a
+  // group; V rows 16 blk + 2 tig + (0, 1, 8, 9), 4 bytes at 4 gid.
+  int k_at[NG], v_at[2][NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    k_at[g] = chunk_at<D>(gid, 2 * g + (tig >> 1)) + 8 * (tig & 1);
+    v_at[0][g] = L::kCodes + chunk_at<D>(2 * tig, 2 * g + (gid >> 2)) + 4 * (gid & 3);
+    v_at[1][g] = L::kCodes + chunk_at<D>(2 * tig + 1, 2 * g + (gid >> 2)) + 4 * (gid & 3);
   }
 
-  // Q^T as the B operand (head gid), and 2^x-scaled sums of q over each group
-  // for this thread's two heads.
-  uint32_t qb[NG][4][2];
-  float qsum[NG][2];
+  // Q^T as the B operand (head gid), scaled; the sums of q that go with the zeros,
+  // in three pieces of the input type (exact to fp32) as the operand of one more
+  // product; the offsets' share for this thread's two heads (2 tig, 2 tig + 1).
+  uint32_t qb[NG][4][2], qz = 0u;
+  float qoff[NG][2], scl[2];
   {
-    const uint16_t* qrow = static_cast<const uint16_t*>(a.q) +
-                           (static_cast<long long>(b) * a.Hq + h0 + gid) * D;
+    const uint4* qrow = reinterpret_cast<const uint4*>(
+        static_cast<const uint16_t*>(a.q) +
+        (static_cast<long long>(b) * a.Hq + h0 + (gid < heads ? gid : 0)) * D + 16 * tig);
+    float big = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint4 x = qrow[8 * g + w];  // dimensions 64 g + 16 tig + 8 w + 0..7
+        if (gid >= heads) x = make_uint4(0, 0, 0, 0);
+        qb[g][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);  // pairs (d, d + 4)
+        qb[g][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
+        qb[g][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+        qb[g][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = qb[g][2 * w + (i >> 1)][i & 1];
+          big = fmaxf(big, fmaxf(fabsf(step_of<BF16>(v)), fabsf(zero_of<BF16>(v))));
+        }
+      }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // 2^k with big 2^k in [128, 256); 1 where q is zero or not finite
+    int k = big > 0.f && big < __int_as_float(0x7f800000)
+                ? 134 - static_cast<int>((__float_as_uint(big) >> 23) & 0xffu)
+                : 0;
+    k = min(max(k, -126), 126);
+    const float f = __int_as_float((127 + k) << 23), inv = __int_as_float((127 - k) << 23);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float sum = 0.f;
+      float even = 0.f, odd = 0.f;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int d = 64 * g + 16 * tig + 8 * (ks >> 1) + 2 * (ks & 1) + e;
-          const uint32_t lo = gid < heads ? qrow[d] : 0u;
-          const uint32_t hi = gid < heads ? qrow[d + 4] : 0u;
-          qb[g][ks][e] = lo | (hi << 16);
-          sum += to_f<BF16>(lo) + to_f<BF16>(hi);
+          const __half2 x = __floats2half2_rn(step_of<BF16>(qb[g][ks][e]) * f,
+                                              zero_of<BF16>(qb[g][ks][e]) * f);
+          qb[g][ks][e] = *reinterpret_cast<const uint32_t*>(&x);
+          (e ? odd : even) += __low2float(x) + __high2float(x);
         }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qsum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig) * a.scale_log2;
-      qsum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4) * a.scale_log2;
+      float sum = even + odd, off = -(kOffEven * even + kOffOdd * odd);
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        off += __shfl_xor_sync(0xffffffffu, off, o);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qoff[g][e] = __shfl_sync(0xffffffffu, off, 8 * tig + 4 * e);
+      // piece tig of the sum, for k = 2 tig + g (one group: k = 2 tig + 1)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t piece = to_16<BF16>(sum);
+        sum -= to_f<BF16>(piece);
+        if (tig == i) qz |= piece << (NG == 2 ? 16 * g : 16);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      scl[e] = __shfl_sync(0xffffffffu, inv, 8 * tig + 4 * e) * a.scale_log2;
   }
   float slope[2] = {0.f, 0.f};
   if constexpr (ALIBI) {
@@ -368,64 +551,94 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
       slope[e] = exp2f(-8.0f * static_cast<float>(h0 + 2 * tig + e + 1) / a.Hq) * kLog2e;
   }
 
-  float m_run[2] = {neg_inf(), neg_inf()}, l_part[2] = {0.f, 0.f};
-  float zacc[NG][2], acc[D / 16][4];
+  float ref[2] = {kNoRef, kNoRef}, l_part[2] = {0.f, 0.f};
+  float zacc[NG][2], ones[NG][4], acc[D / 16][4];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) zacc[g][0] = zacc[g][1] = 0.f;
+  for (int g = 0; g < NG; ++g) {
+    zacc[g][0] = zacc[g][1] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ones[g][e] = 0.f;
+  }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
+  int slot = 0;
   for (; t < s1; t += kWarps * kTile) {
-    const int next = t + kWarps * kTile;
-    float x[2][4];
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[blk][e] = 0.f;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // the tile is there for every lane, and the last one is read
+    fetch(t + (kStages - 1) * kWarps * kTile, slot == 0 ? kStages - 1 : slot - 1);
+    const uint32_t st = ring + slot * L::kStage;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    uint32_t vq[4][NG];  // (s, z) of the V rows gid + 8 i
+    float y[2][4];       // scores in log2 units
+    {
+      float sc[2][NG][4];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t kw[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds<8>(st + k_at[g] + i * 4 * D, kw[i]);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const uint32_t lo = kw[2 * blk][g][w], hi = kw[2 * blk + 1][g][w];
-          mma16816<BF16>(sc, code_pair<BF16, 0>(lo), code_pair<BF16, 0>(hi),
-                         code_pair<BF16, 1>(lo), code_pair<BF16, 1>(hi), qb[g][2 * w][0],
-                         qb[g][2 * w][1]);
-          mma16816<BF16>(sc, code_pair<BF16, 2>(lo), code_pair<BF16, 2>(hi),
-                         code_pair<BF16, 3>(lo), code_pair<BF16, 3>(hi), qb[g][2 * w + 1][0],
-                         qb[g][2 * w + 1][1]);
-        }
+          CodePairs c[4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float s = to_f<BF16>(kq[2 * blk + r][g] & 0xffffu);
-          const float z = to_f<BF16>(kq[2 * blk + r][g] >> 16);
-          const float corr = fmaf(-16.f, s, z), ss = s * a.scale_log2;
+          for (int i = 0; i < 4; ++i) c[i] = code_pairs(kw[i][w]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            x[blk][2 * r + e] += fmaf(ss, sc[2 * r + e], corr * qsum[g][e]);
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+              const CodePairs &lo = c[2 * blk], &hi = c[2 * blk + 1];
+              const uint32_t(&q2)[2] = qb[g][2 * w + half];
+              if (w + half == 0)
+                mma_f16(sc[blk][g], lo.n[0], hi.n[0], lo.n[1], hi.n[1], q2[0], q2[1], qoff[g][0],
+                        qoff[g][1], qoff[g][0], qoff[g][1]);
+              else
+                mma_f16_acc(sc[blk][g], lo.n[2 * half], hi.n[2 * half], lo.n[2 * half + 1],
+                            hi.n[2 * half + 1], q2[0], q2[1]);
+            }
         }
       }
+      uint32_t kq[4][NG];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lds<4 * NG>(st + 2 * L::kCodes + (gid + 8 * i) * 4 * NG, kq[i]);
+        lds<4 * NG>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG, vq[i]);
+      }
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        // the zeros' share: A holds (z of group 0, z of group 1), or (s, z) against (0, q)
+        const uint32_t(&lo)[NG] = kq[2 * blk];
+        const uint32_t(&hi)[NG] = kq[2 * blk + 1];
+        mma_zero<BF16>(y[blk], NG == 2 ? __byte_perm(lo[0], lo[NG - 1], 0x7632) : lo[0],
+                       NG == 2 ? __byte_perm(hi[0], hi[NG - 1], 0x7632) : hi[0], qz);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float s = step_of<BF16>(kq[2 * blk + r][g]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              y[blk][2 * r + e] = fmaf(s, sc[blk][g][2 * r + e], y[blk][2 * r + e]);
+          }
+      }
     }
-    if (next < s1) load_k(next);
+    const bool last = t + kTile > s1;
     if constexpr (ALIBI) {
+      // y scl - slope (n - 1 - row): y carries the bias in its own units
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[blk][e] = fmaf(-slope[e & 1],
-                           static_cast<float>(n - 1 - (t + 16 * blk + 8 * (e >> 1) + gid)),
-                           x[blk][e]);
+          y[blk][e] = fmaf(
+              -slope[e & 1],
+              static_cast<float>(n - 1 - min(t + 16 * blk + 8 * (e >> 1) + gid, s1 - 1)),
+              y[blk][e] * scl[e & 1]);
     }
-    if (t + kTile > s1) {
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (t + 16 * blk + 8 * (e >> 1) + gid >= s1) x[blk][e] = neg_inf();
-    }
-    if (a.scores != nullptr) {  // kept for the gathered weights, log2 units
+    // log2 units: y itself under ALiBi, y scl otherwise
+    const float unit[2] = {ALIBI ? 1.f : scl[0], ALIBI ? 1.f : scl[1]};
+    if (a.scores != nullptr) {  // kept for the gathered weights
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (2 * tig + e < heads) {
@@ -433,80 +646,101 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
                                       a.score_stride + t + gid;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (t + 8 * i + gid < s1) out[8 * i] = x[i >> 1][2 * (i & 1) + e];
+            if (t + 8 * i + gid < s1) out[8 * i] = y[i >> 1][2 * (i & 1) + e] * unit[e];
         }
     }
-    float mx[2];
+    float p[2][4], ps[2][NG][4], sum[2], heavy[2];
+    auto weigh = [&] {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      mx[e] = fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2]));
-    if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kLazy || mx[1] > m_run[1] + kLazy)) {
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[blk][e] = ex2(fmaf(y[blk][e], unit[e & 1], -ref[e & 1]));
+          if (last && t + 16 * blk + 8 * (e >> 1) + gid >= s1) p[blk][e] = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            ps[blk][g][e] = p[blk][e] * step_of<BF16>(vq[2 * blk + (e >> 1)][g]);
+        }
+      // sums of numbers >= 0: past the bound before any of them is far past it
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-        const float m_new = fmaxf(m_run[e], mx[e]);
-        const float alpha = m_new == m_run[e] ? 1.f : ex2(m_run[e] - m_new);
-        m_run[e] = m_new;
+        sum[e] = (p[0][e] + p[0][e + 2]) + (p[1][e] + p[1][e + 2]);
+        heavy[e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          heavy[e] += (ps[0][g][e] + ps[0][g][e + 2]) + (ps[1][g][e] + ps[1][g][e + 2]);
+      }
+    };
+    weigh();
+    if (__any_sync(0xffffffffu, heavy[0] > kMaxWeight || heavy[1] > kMaxWeight ||
+                                    sum[0] > kMaxPlain || sum[1] > kMaxPlain)) {
+      // Raise the reference: the largest p s of these rows becomes about one.  A
+      // row whose step is small beside its zero counts with 2^-12 of the zero, so
+      // that p z stays in range too.
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = neg_inf();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float mag = 0x1p-60f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            mag = fmaxf(mag, fmaxf(step_of<BF16>(vq[i][g]),
+                                   fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f));
+          v = fmaxf(v, fmaf(y[i >> 1][2 * (i & 1) + e], unit[e], __log2f(mag)));
+        }
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        const float r_new = fmaxf(ref[e], v);
+        const float alpha = r_new == ref[e] ? 1.f : ex2(ref[e] - r_new);
+        ref[e] = r_new;
         l_part[e] *= alpha;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) zacc[g][e] *= alpha;
+        for (int g = 0; g < NG; ++g) {
+          zacc[g][e] *= alpha;
+          ones[g][e] *= alpha;
+          ones[g][e + 2] *= alpha;
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           acc[i][e] *= alpha;
           acc[i][e + 2] *= alpha;
         }
       }
+      weigh();
     }
+    l_part[0] += sum[0];
+    l_part[1] += sum[1];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // a row of -inf scores alone leaves m_run at -inf: no weight yet
-        p[e] = x[blk][e] == neg_inf() ? 0.f : ex2(x[blk][e] - m_run[e & 1]);
-        l_part[e & 1] += p[e];
-      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        uint32_t hi[2], lo[2];
+        uint32_t pb[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float s = to_f<BF16>(vq[2 * blk + r][g] & 0xffffu);
-          const float z = to_f<BF16>(vq[2 * blk + r][g] >> 16);
-          const float p0 = p[2 * r] * s, p1 = p[2 * r + 1] * s;
-          const uint32_t h = pack2<true>(p0, p1);
-          const float h0f = __uint_as_float(h << 16), h1f = __uint_as_float(h & 0xffff0000u);
-          const uint32_t l = pack2<true>(p0 - h0f, p1 - h1f);
-          const float r0 = h0f + __uint_as_float(l << 16);
-          const float r1 = h1f + __uint_as_float(l & 0xffff0000u);
-          // what the tensor cores add for the code offset is 16 x the rounded p s
-          zacc[g][0] += fmaf(p[2 * r], z, -16.f * r0);
-          zacc[g][1] += fmaf(p[2 * r + 1], z, -16.f * r1);
-          hi[r] = movmatrix_trans(h);
-          lo[r] = movmatrix_trans(l);
+          const float z = zero_of<BF16>(vq[2 * blk + r][g]);
+          zacc[g][0] = fmaf(p[blk][2 * r], z, zacc[g][0]);
+          zacc[g][1] = fmaf(p[blk][2 * r + 1], z, zacc[g][1]);
+          pb[r] = movmatrix_trans(pack2<false>(ps[blk][g][2 * r], ps[blk][g][2 * r + 1]));
         }
         // rows 2 tig, 2 tig + 1 (first pair) and + 8 (second): words of 8 dimensions
-        const uint32_t w0 = vw[4 * blk][g], w1 = vw[4 * blk + 1][g];
-        const uint32_t w2 = vw[4 * blk + 2][g], w3 = vw[4 * blk + 3][g];
-        const uint32_t xa = __byte_perm(w0, w1, 0x5410), ya = __byte_perm(w0, w1, 0x7632);
-        const uint32_t xb = __byte_perm(w2, w3, 0x5410), yb = __byte_perm(w2, w3, 0x7632);
-#define MEA_KV4_PV(N)                                                                       \
-  {                                                                                         \
-    const uint32_t a0 = code_pair<true, N>(xa), a1 = code_pair<true, N>(ya);                \
-    const uint32_t a2 = code_pair<true, N>(xb), a3 = code_pair<true, N>(yb);                \
-    mma16816<true>(acc[4 * g + N], a0, a1, a2, a3, hi[0], hi[1]);                           \
-    mma16816<true>(acc[4 * g + N], a0, a1, a2, a3, lo[0], lo[1]);                           \
-  }
-        MEA_KV4_PV(0)
-        MEA_KV4_PV(1)
-        MEA_KV4_PV(2)
-        MEA_KV4_PV(3)
-#undef MEA_KV4_PV
+        uint32_t w0, w1, w2, w3;
+        lds<4>(st + v_at[0][g] + blk * 8 * D, &w0);
+        lds<4>(st + v_at[1][g] + blk * 8 * D, &w1);
+        lds<4>(st + v_at[0][g] + blk * 8 * D + 4 * D, &w2);
+        lds<4>(st + v_at[1][g] + blk * 8 * D + 4 * D, &w3);
+        const CodePairs xa = code_pairs(__byte_perm(w0, w1, 0x5410));
+        const CodePairs ya = code_pairs(__byte_perm(w0, w1, 0x7632));
+        const CodePairs xb = code_pairs(__byte_perm(w2, w3, 0x5410));
+        const CodePairs yb = code_pairs(__byte_perm(w2, w3, 0x7632));
+        constexpr uint32_t kOne2 = 0x3C003C00u;
+        mma_f16_acc(ones[g], kOne2, kOne2, kOne2, kOne2, pb[0], pb[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[0], pb[1]);
       }
     }
-    if (next < s1) load_v(next);
   }
 
 #pragma unroll
@@ -517,33 +751,38 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
       for (int g = 0; g < NG; ++g) zacc[g][e] += __shfl_xor_sync(0xffffffffu, zacc[g][e], o);
     }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // the rings are read: their memory joins the warps' states
+  float* c_ref = reinterpret_cast<float*>(smem);
+  float* c_l = c_ref + kWarps * kHeads;
+  float* c_acc = c_l + kWarps * kHeads;
   if (gid == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sm.m[warp][2 * tig + e] = m_run[e];
-      sm.l[warp][2 * tig + e] = l_part[e];
+      c_ref[warp * kHeads + 2 * tig + e] = ref[e];
+      c_l[warp * kHeads + 2 * tig + e] = l_part[e];
     }
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e)  // tile i: dimension 64 (i/4) + 8 gid + i % 4 (+ 4)
-      sm.acc[warp][2 * tig + (e & 1)][64 * (i >> 2) + 8 * gid + (i & 3) + 4 * (e >> 1)] =
-          acc[i][e] + zacc[i >> 2][e & 1];
+      c_acc[(warp * kHeads + 2 * tig + (e & 1)) * D + 64 * (i >> 2) + 8 * gid + (i & 3) +
+            4 * (e >> 1)] =
+          fmaf((i & 1) ? -kOffOdd : -kOffEven, ones[i >> 2][e], acc[i][e]) + zacc[i >> 2][e & 1];
   __syncthreads();
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
     const int g = idx / D, d = idx - g * D;
-    float mx = neg_inf();
+    float mx = kNoRef;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][g]);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, c_ref[w * kHeads + g]);
     float lsum = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float wgt = sm.m[w][g] == neg_inf() ? (sm.l[w][g] == 0.f ? 0.f : 1.f)
-                                                : ex2(sm.m[w][g] - mx);
-      lsum += wgt * sm.l[w][g];
-      o += wgt * sm.acc[w][g][d];
+      const float wgt = ex2(c_ref[w * kHeads + g] - mx);  // 1 if no warp has a reference
+      lsum = fmaf(wgt, c_l[w * kHeads + g], lsum);
+      o = fmaf(wgt, c_acc[(w * kHeads + g) * D + d], o);
     }
     const long long row = static_cast<long long>(b) * a.Hq + h0 + g;
     const float val = lsum == 0.f ? 0.f : o / lsum;  // a NaN stays a NaN
@@ -661,9 +900,14 @@ template <int D, bool BF16>
 cudaError_t decode_t(const Kv4DecodeArgs& a, bool alibi, cudaStream_t stream) {
   if (a.max_splits > 0) {
     const dim3 grid(a.max_splits, a.Hkv * a.head_blocks, a.B);
-    if (alibi) kv4_decode_kernel<D, BF16, true><<<grid, kThreads, 0, stream>>>(a);
-    else kv4_decode_kernel<D, BF16, false><<<grid, kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    constexpr auto with = kv4_decode_kernel<D, BF16, true>;
+    constexpr auto without = kv4_decode_kernel<D, BF16, false>;
+    cudaError_t e = alibi ? set_smem_once<with>(KSmem<D>::kBytes)
+                          : set_smem_once<without>(KSmem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (alibi) with<<<grid, kThreads, KSmem<D>::kBytes, stream>>>(a);
+    else without<<<grid, kThreads, KSmem<D>::kBytes, stream>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (a.part_o == nullptr && a.max_splits > 0 && a.w_out == nullptr) return cudaSuccess;
@@ -681,7 +925,7 @@ int kv4_weight_rows() { return kWeightRows; }
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, bool bf16,
                               cudaStream_t stream) {
   const long long per = static_cast<long long>(kRowUnroll) * kRowThreads * 8 / head_dim;
-  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per), 2);
+  const dim3 grid(static_cast<unsigned>((a.order.total + per - 1) / per), 2);
   if (head_dim == 64 && !bf16) kv4_append_kernel<64, false><<<grid, kRowThreads, 0, stream>>>(a);
   else if (head_dim == 64) kv4_append_kernel<64, true><<<grid, kRowThreads, 0, stream>>>(a);
   else if (!bf16) kv4_append_kernel<128, false><<<grid, kRowThreads, 0, stream>>>(a);
@@ -691,7 +935,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, bool bf16,
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int head_dim, bool bf16, cudaStream_t stream) {
   const long long per = static_cast<long long>(kRowUnroll) * kRowThreads * 8 / head_dim;
-  const dim3 grid(static_cast<unsigned>((a.total + per - 1) / per), 2);
+  const dim3 grid(static_cast<unsigned>((a.order.total + per - 1) / per), 2);
   if (head_dim == 64 && !bf16) kv4_read_kernel<64, false><<<grid, kRowThreads, 0, stream>>>(a);
   else if (head_dim == 64) kv4_read_kernel<64, true><<<grid, kRowThreads, 0, stream>>>(a);
   else if (!bf16) kv4_read_kernel<128, false><<<grid, kRowThreads, 0, stream>>>(a);
