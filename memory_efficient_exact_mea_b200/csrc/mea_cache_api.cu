@@ -8,6 +8,12 @@
 #include "mea.h"
 #include "mea_internal.h"
 
+#ifndef MEA_CHUNK
+#define MEA_CHUNK 1024
+#endif
+#ifndef MEA_FILL
+#define MEA_FILL 6
+#endif
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -46,9 +52,9 @@ DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
   DecodePlan p{};
   p.head_blocks = (Hq / Hkv + 7) / 8;
   const int64_t units = static_cast<int64_t>(B) * Hkv * p.head_blocks;
-  const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
+  const int64_t want = std::max<int64_t>(1, 148 * MEA_FILL / std::max<int64_t>(1, units));
   int64_t chunk = (max_len + want - 1) / want;
-  chunk = std::min<int64_t>(1024, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  chunk = std::min<int64_t>(MEA_CHUNK, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);
   return p;

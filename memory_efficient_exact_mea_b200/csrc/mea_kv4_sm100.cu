@@ -266,15 +266,16 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 //   q.k^_j = sum_g s_jg (sum_{d in g} q_d c_jd) + z_jg (sum_{d in g} q_d)
 //   out_d  = sum_j (p_j s_jg) c_jd + sum_j p_j z_jg          (d in group g)
 // so the codes go into the tensor cores as they are, and no dequantised value is
-// ever formed.  A nibble in mantissa bits [b, b + 4) of an fp16 number of exponent
-// 10 - b makes that number 2^(10 - b) + c exactly: two shifts and four and-ors turn
-// a word into four operand pairs, with offsets 256 (b = 2) and 16 (b = 6).  The
-// offsets are taken off again exactly: Q.K^T starts its accumulator at minus their
-// share, and P.V has one more accumulator whose A operand is all ones, the sum of
-// the very P values that were multiplied.
+// ever formed.  A nibble alone in the low byte of an fp16 number is a subnormal: in
+// bits 0-3 the number c 2^-24, in bits 4-7 the number c 2^-20, both exact.  So one
+// shift and four ands turn a word into four operand pairs, and the powers of two go
+// into q (one half of its operand is 16 times larger) and into the final scaling.
+// (With 16 + c and 256 + c in the mantissa instead -- two shifts, four and-ors whose
+// second constant costs a register or an instruction, one more product for the sum
+// of the weights -- the decode of B = 64 took 101 us.)
 //
-// Both products run in fp16 whatever the input type.  q is scaled by a power of two
-// to a largest magnitude in [128, 256], exact but for values 2^-22 of that and less.
+// Both products run in fp16 whatever the input type.  q is scaled by a power of two to
+// a largest magnitude below 256, exact but for values 2^-22 of that and less.
 // P' = p s is rounded to fp16 (11 bits, finer than a bf16 result's 8; mea_decode
 // rounds p the same way for fp16): the reference R of p = 2^(y - R) is chosen per
 // head so that the largest p s is about one, not the largest p, and is raised only
@@ -287,6 +288,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // rows' words.  Each warp copies its own tiles into a ring of its own (cp.async,
 // 16-byte chunks, no barrier but __syncwarp), two tiles ahead.
 // ---------------------------------------------------------------------------
+#ifndef MEA_OCC
+#define MEA_OCC 4
+#endif
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;        // rows per warp and iteration
@@ -330,16 +334,15 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// Nibbles N and N + 4 of a word as fp16 pairs: offset 256 for even N, 16 for odd.
+// Nibbles N and N + 4 of a word as fp16 pairs: c 2^-24 for even N, c 2^-20 for odd.
 struct CodePairs {
   uint32_t n[4];
 };
 __device__ __forceinline__ CodePairs code_pairs(uint32_t w) {
-  const uint32_t lo = w << 2, hi = w >> 6;
-  return {{(lo & 0x003C003Cu) | 0x5C005C00u, (lo & 0x03C003C0u) | 0x4C004C00u,
-           (hi & 0x003C003Cu) | 0x5C005C00u, (hi & 0x03C003C0u) | 0x4C004C00u}};
+  const uint32_t hi = w >> 8;
+  return {{w & 0x000F000Fu, w & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u}};
 }
-constexpr float kOffEven = 256.f, kOffOdd = 16.f;
+constexpr float kUnitEven = 0x1p24f, kUnitOdd = 0x1p20f;  // what brings them back to c
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -351,11 +354,14 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
 }
 
 template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t* r) {
-  if constexpr (BYTES == 8)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-  else
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t* r) {
+  if constexpr (BYTES == 8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    r[0] = x.x;
+    r[1] = x.y;
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 template <bool BF16>
@@ -370,7 +376,7 @@ __device__ __forceinline__ float zero_of(uint32_t w) {  // high 16 bits
   else return __high2float(*reinterpret_cast<const __half2*>(&w));
 }
 
-constexpr int kStages = 3;  // ring of one warp: two tiles in flight, one in use
+constexpr int kStages = 3;  // ring of one warp: one tile in use, two in flight
 
 template <int D>
 struct KSmem {
@@ -396,7 +402,7 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 }
 
 template <int D, bool BF16, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, MEA_OCC) kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = KSmem<D>;
   constexpr int NG = L::NG;  // groups of a row
   extern __shared__ __align__(128) uint8_t smem[];
@@ -430,14 +436,15 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_codes) + plane * (D / 2);
   const uint8_t* kp = static_cast<const uint8_t*>(a.k_params) + plane * (4 * NG);
   const uint8_t* vp = static_cast<const uint8_t*>(a.v_params) + plane * (4 * NG);
-  const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+  uint8_t* const ring = smem + warp * L::kWarp;
+  const uint32_t ring_u32 = smem_u32(ring);
 
   // One tile into stage `slot`; in the last tile, rows past the end take the last
   // row again (their weight is zero).
   constexpr int kPer = D / 32;  // 16-byte chunks of a row's codes; 8 or 16 rows a copy
   const int chunk0 = chunk_at<D>(lane / kPer, lane % kPer);
   auto fetch = [&](int tile, int slot) {
-    const uint32_t st = ring + slot * L::kStage, to = st + chunk0;
+    const uint32_t st = ring_u32 + slot * L::kStage, to = st + chunk0;
     const uint32_t top = st + 2 * L::kCodes + lane * 4 * NG;
     if (tile + kTile <= s1) {
       const long long off = static_cast<long long>(tile) * (D / 2) + lane * 16;
@@ -480,58 +487,55 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
 
   // Q^T as the B operand (head gid), scaled; the sums of q that go with the zeros,
   // in three pieces of the input type (exact to fp32) as the operand of one more
-  // product; the offsets' share for this thread's two heads (2 tig, 2 tig + 1).
+  // product.
   uint32_t qb[NG][4][2], qz = 0u;
-  float qoff[NG][2], scl[2];
+  float scl[2];
   {
     const uint4* qrow = reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(a.q) +
         (static_cast<long long>(b) * a.Hq + h0 + (gid < heads ? gid : 0)) * D + 16 * tig);
-    float big = 0.f;
+    uint32_t big2 = 0u;  // largest magnitudes, as pairs of bit patterns
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint4 x = qrow[8 * g + w];  // dimensions 64 g + 16 tig + 8 w + 0..7
         if (gid >= heads) x = make_uint4(0, 0, 0, 0);
+        big2 = __vmaxu2(__vmaxu2(big2, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                        __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
         qb[g][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);  // pairs (d, d + 4)
         qb[g][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
         qb[g][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
         qb[g][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v = qb[g][2 * w + (i >> 1)][i & 1];
-          big = fmaxf(big, fmaxf(fabsf(step_of<BF16>(v)), fabsf(zero_of<BF16>(v))));
-        }
       }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    // 2^k with big 2^k in [128, 256); 1 where q is zero or not finite
-    int k = big > 0.f && big < __int_as_float(0x7f800000)
-                ? 134 - static_cast<int>((__float_as_uint(big) >> 23) & 0xffu)
-                : 0;
+    big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 1));
+    big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
+    const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
+    // 2^k with the largest |q| 2^k in [128, 256), 1 where q is zero or not finite; fp16
+    // numbers are only made smaller (their sums, in fp16 pieces, must fit)
+    int k = 0;
+    if (BF16 && big != 0u && big < 0x7f80u) k = 134 - static_cast<int>(big >> 7);
+    if (!BF16 && big < 0x7c00u) k = min(22 - static_cast<int>(big >> 10), 0);
     k = min(max(k, -126), 126);
     const float f = __int_as_float((127 + k) << 23), inv = __int_as_float((127 - k) << 23);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float even = 0.f, odd = 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const __half2 x = __floats2half2_rn(step_of<BF16>(qb[g][ks][e]) * f,
-                                              zero_of<BF16>(qb[g][ks][e]) * f);
+          if constexpr (BF16)
+            qb[g][ks][e] = pack2<false>(step_of<true>(qb[g][ks][e]) * f,
+                                        zero_of<true>(qb[g][ks][e]) * f);
+          __half2 x = *reinterpret_cast<const __half2*>(&qb[g][ks][e]);
+          if constexpr (!BF16) x = __hmul2(x, __float2half2_rn(f));
+          sum += __low2float(x) + __high2float(x);
+          if (e == 0) x = __hmul2(x, __float2half2_rn(kUnitEven / kUnitOdd));
           qb[g][ks][e] = *reinterpret_cast<const uint32_t*>(&x);
-          (e ? odd : even) += __low2float(x) + __high2float(x);
         }
-      float sum = even + odd, off = -(kOffEven * even + kOffOdd * odd);
 #pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        off += __shfl_xor_sync(0xffffffffu, off, o);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) qoff[g][e] = __shfl_sync(0xffffffffu, off, 8 * tig + 4 * e);
+      for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       // piece tig of the sum, for k = 2 tig + g (one group: k = 2 tig + 1)
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
@@ -552,78 +556,82 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
   }
 
   float ref[2] = {kNoRef, kNoRef}, l_part[2] = {0.f, 0.f};
-  float zacc[NG][2], ones[NG][4], acc[D / 16][4];
+  float zacc[NG][2], acc[D / 16][4];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     zacc[g][0] = zacc[g][1] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ones[g][e] = 0.f;
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
-  int slot = 0;
-  for (; t < s1; t += kWarps * kTile) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncwarp();  // the tile is there for every lane, and the last one is read
-    fetch(t + (kStages - 1) * kWarps * kTile, slot == 0 ? kStages - 1 : slot - 1);
-    const uint32_t st = ring + slot * L::kStage;
-    slot = slot == kStages - 1 ? 0 : slot + 1;
-    uint32_t vq[4][NG];  // (s, z) of the V rows gid + 8 i
-    float y[2][4];       // scores in log2 units
-    {
-      float sc[2][NG][4];
+  // Scores of the tile in `slot` times the scale of q.
+  auto score = [&](int slot, float(&y)[2][4]) {
+    const uint8_t* st = ring + slot * L::kStage;
+    float sc[2][NG][4];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint32_t kw[4][2];
+    for (int g = 0; g < NG; ++g) {
+      uint32_t kw[4][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lds<8>(st + k_at[g] + i * 4 * D, kw[i]);
+      for (int i = 0; i < 4; ++i) lds<8>(st + k_at[g] + i * 4 * D, kw[i]);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          CodePairs c[4];
+      for (int w = 0; w < 2; ++w) {
+        CodePairs c[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = code_pairs(kw[i][w]);
+        for (int i = 0; i < 4; ++i) c[i] = code_pairs(kw[i][w]);
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-              const CodePairs &lo = c[2 * blk], &hi = c[2 * blk + 1];
-              const uint32_t(&q2)[2] = qb[g][2 * w + half];
-              if (w + half == 0)
-                mma_f16(sc[blk][g], lo.n[0], hi.n[0], lo.n[1], hi.n[1], q2[0], q2[1], qoff[g][0],
-                        qoff[g][1], qoff[g][0], qoff[g][1]);
-              else
-                mma_f16_acc(sc[blk][g], lo.n[2 * half], hi.n[2 * half], lo.n[2 * half + 1],
-                            hi.n[2 * half + 1], q2[0], q2[1]);
-            }
-        }
-      }
-      uint32_t kq[4][NG];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lds<4 * NG>(st + 2 * L::kCodes + (gid + 8 * i) * 4 * NG, kq[i]);
-        lds<4 * NG>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG, vq[i]);
-      }
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        // the zeros' share: A holds (z of group 0, z of group 1), or (s, z) against (0, q)
-        const uint32_t(&lo)[NG] = kq[2 * blk];
-        const uint32_t(&hi)[NG] = kq[2 * blk + 1];
-        mma_zero<BF16>(y[blk], NG == 2 ? __byte_perm(lo[0], lo[NG - 1], 0x7632) : lo[0],
-                       NG == 2 ? __byte_perm(hi[0], hi[NG - 1], 0x7632) : hi[0], qz);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float s = step_of<BF16>(kq[2 * blk + r][g]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              y[blk][2 * r + e] = fmaf(s, sc[blk][g][2 * r + e], y[blk][2 * r + e]);
+          for (int blk = 0; blk < 2; ++blk) {
+            const CodePairs &lo = c[2 * blk], &hi = c[2 * blk + 1];
+            const uint32_t(&q2)[2] = qb[g][2 * w + half];
+            if (w + half == 0)
+              mma_f16(sc[blk][g], lo.n[0], hi.n[0], lo.n[1], hi.n[1], q2[0], q2[1], 0.f, 0.f, 0.f,
+                      0.f);
+            else
+              mma_f16_acc(sc[blk][g], lo.n[2 * half], hi.n[2 * half], lo.n[2 * half + 1],
+                          hi.n[2 * half + 1], q2[0], q2[1]);
           }
       }
     }
+    uint32_t kq[4][NG];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lds<4 * NG>(st + 2 * L::kCodes + (gid + 8 * i) * 4 * NG, kq[i]);
+    }
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+      // the zeros' share: A holds (z of group 0, z of group 1), or (s, z) against (0, q)
+      const uint32_t(&lo)[NG] = kq[2 * blk];
+      const uint32_t(&hi)[NG] = kq[2 * blk + 1];
+      mma_zero<BF16>(y[blk], NG == 2 ? __byte_perm(lo[0], lo[NG - 1], 0x7632) : lo[0],
+                     NG == 2 ? __byte_perm(hi[0], hi[NG - 1], 0x7632) : hi[0], qz);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float s = step_of<BF16>(kq[2 * blk + r][g]) * kUnitOdd;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            y[blk][2 * r + e] = fmaf(s, sc[blk][g][2 * r + e], y[blk][2 * r + e]);
+        }
+    }
+  };
+
+  int slot = 0;
+  for (; t < s1; t += kWarps * kTile) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // the tile is there for every lane, and the one before is read
+    fetch(t + (kStages - 1) * kWarps * kTile, slot == 0 ? kStages - 1 : slot - 1);
+    const uint8_t* st = ring + slot * L::kStage;
+    float y[2][4];
+    score(slot, y);
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    uint32_t vq[4][NG];  // (s, z) of the V rows gid + 8 i
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      lds<4 * NG>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG, vq[i]);
     const bool last = t + kTile > s1;
     if constexpr (ALIBI) {
       // y scl - slope (n - 1 - row): y carries the bias in its own units
@@ -649,26 +657,39 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
             if (t + 8 * i + gid < s1) out[8 * i] = y[i >> 1][2 * (i & 1) + e] * unit[e];
         }
     }
-    float p[2][4], ps[2][NG][4], sum[2], heavy[2];
+    // Weights of the tile against the present reference: p s in fp16, and the sums
+    // of p, p s and p z (an overflow shows in a sum of numbers >= 0).
+    uint32_t pk[2][NG][2];
+    float sum[2], heavy[2], zsum[NG][2];
     auto weigh = [&] {
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[blk][e] = ex2(fmaf(y[blk][e], unit[e & 1], -ref[e & 1]));
-          if (last && t + 16 * blk + 8 * (e >> 1) + gid >= s1) p[blk][e] = 0.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            ps[blk][g][e] = p[blk][e] * step_of<BF16>(vq[2 * blk + (e >> 1)][g]);
-        }
-      // sums of numbers >= 0: past the bound before any of them is far past it
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sum[e] = (p[0][e] + p[0][e + 2]) + (p[1][e] + p[1][e + 2]);
-        heavy[e] = 0.f;
+        sum[e] = heavy[e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-          heavy[e] += (ps[0][g][e] + ps[0][g][e + 2]) + (ps[1][g][e] + ps[1][g][e + 2]);
+        for (int g = 0; g < NG; ++g) zsum[g][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // row gid + 8 i
+        float p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          p[e] = ex2(fmaf(y[i >> 1][2 * (i & 1) + e], unit[e], -ref[e]));
+        if (last) {
+          asm volatile("" ::: "memory");  // a branch, not selects in every tile
+          if (t + 8 * i + gid >= s1) p[0] = p[1] = 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float s = step_of<BF16>(vq[i][g]), z = zero_of<BF16>(vq[i][g]);
+          const float ps0 = p[0] * s, ps1 = p[1] * s;
+          heavy[0] += ps0;
+          heavy[1] += ps1;
+          zsum[g][0] = fmaf(p[0], z, zsum[g][0]);
+          zsum[g][1] = fmaf(p[1], z, zsum[g][1]);
+          pk[i >> 1][g][i & 1] = pack2<false>(ps0, ps1);
+        }
+        sum[0] += p[0];
+        sum[1] += p[1];
       }
     };
     weigh();
@@ -699,8 +720,6 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           zacc[g][e] *= alpha;
-          ones[g][e] *= alpha;
-          ones[g][e + 2] *= alpha;
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -713,17 +732,14 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
     l_part[0] += sum[0];
     l_part[1] += sum[1];
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
+    for (int g = 0; g < NG; ++g) {
+      zacc[g][0] += zsum[g][0];
+      zacc[g][1] += zsum[g][1];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int blk = 0; blk < 2; ++blk) {
         uint32_t pb[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float z = zero_of<BF16>(vq[2 * blk + r][g]);
-          zacc[g][0] = fmaf(p[blk][2 * r], z, zacc[g][0]);
-          zacc[g][1] = fmaf(p[blk][2 * r + 1], z, zacc[g][1]);
-          pb[r] = movmatrix_trans(pack2<false>(ps[blk][g][2 * r], ps[blk][g][2 * r + 1]));
-        }
+        pb[0] = movmatrix_trans(pk[blk][g][0]);
+        pb[1] = movmatrix_trans(pk[blk][g][1]);
         // rows 2 tig, 2 tig + 1 (first pair) and + 8 (second): words of 8 dimensions
         uint32_t w0, w1, w2, w3;
         lds<4>(st + v_at[0][g] + blk * 8 * D, &w0);
@@ -734,8 +750,6 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
         const CodePairs ya = code_pairs(__byte_perm(w0, w1, 0x7632));
         const CodePairs xb = code_pairs(__byte_perm(w2, w3, 0x5410));
         const CodePairs yb = code_pairs(__byte_perm(w2, w3, 0x7632));
-        constexpr uint32_t kOne2 = 0x3C003C00u;
-        mma_f16_acc(ones[g], kOne2, kOne2, kOne2, kOne2, pb[0], pb[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[0], pb[1]);
@@ -769,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
     for (int e = 0; e < 4; ++e)  // tile i: dimension 64 (i/4) + 8 gid + i % 4 (+ 4)
       c_acc[(warp * kHeads + 2 * tig + (e & 1)) * D + 64 * (i >> 2) + 8 * gid + (i & 3) +
             4 * (e >> 1)] =
-          fmaf((i & 1) ? -kOffOdd : -kOffEven, ones[i >> 2][e], acc[i][e]) + zacc[i >> 2][e & 1];
+          fmaf(acc[i][e], (i & 1) ? kUnitOdd : kUnitEven, zacc[i >> 2][e & 1]);
   __syncthreads();
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {

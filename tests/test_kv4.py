@@ -255,6 +255,32 @@ def test_decode_moving_maximum(mea, dtype):
     check_decode(mea, cache, q, [n], K ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,mag", [("f16", 30000.0), ("f16", 6e-6), ("bf16", 1e30),
+                                       ("bf16", 1e-30)])
+def test_decode_q_of_any_size(mea, dtype, mag):
+    """q near the ends of its type's range, the scale making up for it."""
+    lens, K = [200, 77], 128
+    cache = make_cache(mea, lens, 210, 2, K, dtype)
+    q = (torch.rand(2, 4, K, generator=gen(31)) * 2 - 1)
+    q = (q.abs() + 0.5 if mag in (30000.0, 1e30) else q) * (mag / 1.5)
+    check_decode(mea, cache, q.to(DT[dtype]), lens, K ** -0.5 / mag)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_decode_steps_of_many_sizes(mea, dtype):
+    """Rows whose values differ by factors up to 2^16, so that the reference of the weights
+    moves with the steps as well as with the scores."""
+    n, K = 500, 64
+    size = torch.exp2(torch.randint(-8, 9, (1, n, 1, 1), generator=gen(41)).float())
+    k = torch.randn(1, n, 1, K, generator=gen(42)).to(DT[dtype])
+    v = (torch.randn(1, n, 1, K, generator=gen(43)) * size).to(DT[dtype])
+    v[0, 100:140] = 3.0  # steps of zero
+    cache = mea.mea_kv4_alloc(1, n, 1, K, DT[dtype], DEV)
+    mea.mea_kv4_append(k.to(DEV), v.to(DEV), cache, i32([0]))
+    q = torch.randn(1, 3, K, generator=gen(44)).to(DT[dtype])
+    check_decode(mea, cache, q, [n], K ** -0.5)
+
+
 def test_decode_scale_zero_and_steps_of_zero(mea):
     cache = mea.mea_kv4_alloc(1, 50, 1, 64, torch.float16, DEV)
     k = torch.full((1, 50, 1, 64), 2.0).half()
