@@ -28,13 +28,11 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
-// Up to 8 rows of a head at a time; false if the batch has 2^31 rows or more.
+// False if the batch has 2^31 rows or more.
 bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
-  o->shift = M >= 8 ? 3 : M >= 4 ? 2 : M >= 2 ? 1 : 0;
-  const int64_t tiles = (static_cast<int64_t>(M) + (1 << o->shift) - 1) >> o->shift;
-  const int64_t per = tiles << o->shift;
-  if (static_cast<int64_t>(B) * Hkv > kMaxRows / per) return false;
-  o->total = static_cast<uint32_t>(per * B * Hkv);
+  const int64_t tiles = (static_cast<int64_t>(M) + mea::kv4_row_group() - 1) / mea::kv4_row_group();
+  if (static_cast<int64_t>(B) * Hkv > kMaxRows / (tiles * mea::kv4_row_group())) return false;
+  o->total = static_cast<uint32_t>(tiles * B * Hkv);
   o->heads = mea::fast_div(static_cast<uint32_t>(Hkv));
   o->tiles = mea::fast_div(static_cast<uint32_t>(tiles));
   return true;
@@ -143,6 +141,9 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
                                                                               : MEA_ERR_CUDA;
 }
 
+// Scores of one head: rows rounded up to whole 16-byte loads.
+static size_t score_stride(int max_len) { return (static_cast<size_t>(max_len) + 3) & ~size_t(3); }
+
 // Workspace: partial outputs, partial log-sum-exps (both only with several
 // splits or weights), scores (weights only), each 256-byte aligned.
 static size_t kv4_workspace(int B, int Hq, int Hkv, int K, int max_len, bool weights,
@@ -154,7 +155,7 @@ static size_t kv4_workspace(int B, int Hq, int Hkv, int K, int max_len, bool wei
   *lse_at = at;
   if (p.splits > 1 || weights) at += align256(rows * p.splits * sizeof(float));
   *score_at = at;
-  if (weights) at += align256(rows * static_cast<size_t>(max_len) * sizeof(float));
+  if (weights) at += align256(rows * score_stride(max_len) * sizeof(float));
   return at;
 }
 
@@ -210,7 +211,7 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
   a.part_o = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   a.part_lse = p.splits > 1 || weights_out ? reinterpret_cast<float*>(ws + lse_at) : nullptr;
   a.scores = weights_out ? reinterpret_cast<float*>(ws + score_at) : nullptr;
-  a.score_stride = max_kv_len;
+  a.score_stride = static_cast<long long>(score_stride(max_kv_len));
   a.w_in = weights_in;
   a.w_out = weights_out;
   a.B = B;
@@ -364,6 +365,7 @@ int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weight
   // other memory the rows are shared out; in place a piece's rows are one block's,
   // so narrow pieces make the parallelism when there are few (sequence, head)s.
   const int64_t bh = static_cast<int64_t>(B) * Hkv;
+  a.in_place = in_place;
   a.seg_rows = in_place ? budget : std::max(256, (budget + 65534) / 65535);
   const int64_t segs = (budget + a.seg_rows - 1) / a.seg_rows;
   int pieces = 0;

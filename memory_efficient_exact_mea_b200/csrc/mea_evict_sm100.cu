@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
 
 template <int A>
 struct Word;
@@ -187,37 +186,62 @@ __device__ __forceinline__ void store_word(uint8_t* p, const Word<A>& w) {
     *reinterpret_cast<uint32_t*>(p) = w.v[0];
 }
 
-template <int A>
-__device__ void move_rows(const EvictPlane& pl, const uint8_t* src, uint8_t* dst,
-                          const int32_t* kept, int r_begin, int r_end) {
+// Rows [r_begin, r_end) of one column piece.  In place, a tile's sources lie at or
+// past the tile, so one barrier between its loads and its stores orders everything;
+// the next tile's loads go out before this one's stores.
+template <int A, bool IN_PLACE>
+__device__ __forceinline__ void move_rows(const EvictPlane& pl, const uint8_t* src, uint8_t* dst,
+                                          const int32_t* kept, int r_begin, int r_end) {
+  constexpr int U = IN_PLACE ? 8 : 4;
   const int lanes = pl.piece_bytes / A;
   const int part = threadIdx.x % lanes, sub = threadIdx.x / lanes;
   const int per = kMoveThreads / lanes;  // rows per unroll step
-  const int tile = per * kMoveUnroll;
   const bool mine = sub < per;
-  Word<A> cur[kMoveUnroll], nxt[kMoveUnroll];
-  auto fetch = [&](Word<A>(&w)[kMoveUnroll], int r0) {
+  src += part * A;
+  dst += part * A;
+  if constexpr (!IN_PLACE) {
+    for (int r0 = r_begin; r0 < r_end; r0 += per * U) {
+      int32_t from[U];
+      Word<A> w[U];
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int r = r0 + u * per + sub;
-      if (mine && r < r_end)
-        w[u] = load_word<A>(src + kept[r] * pl.src_s[1] + part * A);
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * per + sub;
+        from[u] = mine && r < r_end ? kept[r] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (from[u] >= 0) w[u] = load_word<A>(src + from[u] * pl.src_s[1]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (from[u] >= 0) store_word<A>(dst + (r0 + u * per + sub) * pl.dst_s[1], w[u]);
     }
-  };
-  fetch(cur, r_begin);
-  for (int r0 = r_begin; r0 < r_end; r0 += tile) {
-    fetch(nxt, r0 + tile);  // sources from row r0 + tile on: this tile's stores end there
-    __syncthreads();
+  } else {
+    Word<A> cur[U], nxt[U];
+    auto fetch = [&](Word<A>(&w)[U], int r0) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int r = r0 + u * per + sub;
-      if (mine && r < r_end) store_word<A>(dst + r * pl.dst_s[1] + part * A, cur[u]);
-      cur[u] = nxt[u];
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * per + sub;
+        if (mine && r < r_end) w[u] = load_word<A>(src + kept[r] * pl.src_s[1]);
+      }
+    };
+    fetch(cur, r_begin);
+    for (int r0 = r_begin; r0 < r_end; r0 += per * U) {
+      fetch(nxt, r0 + per * U);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * per + sub;
+        if (mine && r < r_end) store_word<A>(dst + r * pl.dst_s[1], cur[u]);
+        cur[u] = nxt[u];
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  grid_dependency_wait();
   int p = 0;
   while (p + 1 < a.n_planes && static_cast<int>(blockIdx.x) >= a.first_block[p + 1]) ++p;
   const EvictPlane& pl = a.planes[p];
@@ -233,9 +257,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   // in place, a sequence within its budget stays where it is
   if (r_begin < r_end && !(pl.src == pl.dst && n <= a.budget)) {
     const int32_t* kept = a.kept + static_cast<long long>(bh) * a.budget;
-    if (pl.access == 16) move_rows<16>(pl, src, dst, kept, r_begin, r_end);
-    else if (pl.access == 8) move_rows<8>(pl, src, dst, kept, r_begin, r_end);
-    else move_rows<4>(pl, src, dst, kept, r_begin, r_end);
+    if (pl.access == 16) move_rows<16, IN_PLACE>(pl, src, dst, kept, r_begin, r_end);
+    else if (pl.access == 8) move_rows<8, IN_PLACE>(pl, src, dst, kept, r_begin, r_end);
+    else move_rows<4, IN_PLACE>(pl, src, dst, kept, r_begin, r_end);
   }
   if (pl.dst == reinterpret_cast<uint8_t*>(a.w_out) && blockIdx.z == 0) {
     __syncthreads();  // in place: after the weights have moved down
@@ -252,8 +276,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const dim3 grid(a.first_block[a.n_planes], a.B * a.Hkv,
                   (a.budget + a.seg_rows - 1) / a.seg_rows);
-  evict_move_kernel<<<grid, kMoveThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.in_place ? evict_move_kernel<true> : evict_move_kernel<false>, grid,
+                      kMoveThreads, 0, stream, a);
 }
 
 }  // namespace mea

@@ -3,7 +3,7 @@
 #pragma once
 
 #include <cuda.h>
-#include <cuda_runtime_api.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -26,6 +26,25 @@ cudaError_t set_smem_once(int bytes) {
   e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_acq_rel);
   return e;
+}
+
+// Launches `kern` so that its blocks may start while the stream's previous kernel is
+// still running (programmatic dependent launch): the kernel waits for that kernel's
+// results itself (grid_dependency_wait), and the launch's own latency is hidden.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Prefill: one CTA computes two 128-row query tiles of one (sequence, head).
@@ -161,10 +180,10 @@ inline FastDiv fast_div(uint32_t d) {
   return f;
 }
 
-// Flat order of (sequence, row, head): 2^shift rows of a head, next head, next rows.
+// Flat order of (sequence, row group, head), the head fastest.
 struct RowOrder {
-  FastDiv heads, tiles;
-  uint32_t shift, total;  // total < 2^31
+  FastDiv heads, tiles;  // heads; row groups of a sequence
+  uint32_t total;        // < 2^31
 };
 
 struct Kv4AppendArgs {
@@ -209,7 +228,8 @@ struct Kv4DecodeArgs {
   float scale_log2;
 };
 
-int kv4_weight_rows();
+int kv4_weight_rows();  // rows of one weight block of the merge launch
+int kv4_row_group();    // rows of one head a group of lanes stores or loads
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, bool bf16,
                               cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int head_dim, bool bf16, cudaStream_t stream);
@@ -263,6 +283,7 @@ struct EvictArgs {
   int first_block[kMaxPlanes + 1];  // plane p: pieces first_block[p] .. first_block[p + 1] - 1
   int n_planes;
   int seg_rows;              // kept rows one move block takes (budget when anything is in place)
+  bool in_place;             // some plane or the weights
   const float* weights;      // [B, Hkv, cap]
   float* w_out;              // [B, Hkv, out_rows]
   const int32_t* lens;       // [B]

@@ -36,35 +36,24 @@ __device__ __forceinline__ uint32_t to_16(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows of a [B, M, Hkv] batch in one flat order: a few rows (2^shift) of one head,
-// then the next head, then the next rows.  A block's share is then one contiguous
-// piece of the 16-bit side ([B, M, Hkv, K]) and runs of a few whole rows on the
-// 4-bit side ([B, Hkv, rows, ...]), whatever M is.  (Head by head, 2 KB apart on the
-// 16-bit side, the same kernels took 1.5 to 2 times as long.)
+// Rows of a [B, M, Hkv] batch in one flat order: kRowGroup rows of one head (one
+// group of lanes takes them all), then the next head, then the next rows.  A
+// block's share is one contiguous piece of the 16-bit side ([B, M, Hkv, K]) and
+// runs of a few whole rows on the 4-bit side ([B, Hkv, rows, ...]).  (Head by head,
+// 2 KB apart on the 16-bit side, loading 300 MB took 87 us instead of 78; a row at
+// a time, its place divided out for each, left the kernels bound by that
+// arithmetic.)
 // ---------------------------------------------------------------------------
-struct RowAt {
-  unsigned b, h, r;
-};
+constexpr int kRowThreads = 256;
+constexpr int kRowGroup = 4;
+
 __device__ __forceinline__ unsigned divide(unsigned x, const FastDiv& d) {
   return (__umulhi(x, d.m) + x) >> d.s;
 }
-__device__ __forceinline__ RowAt row_at(unsigned i, const RowOrder& o) {
-  RowAt x;
-  const unsigned q = i >> o.shift;
-  const unsigned q2 = divide(q, o.heads);
-  x.h = q - q2 * o.heads.d;
-  x.b = divide(q2, o.tiles);
-  x.r = ((q2 - x.b * o.tiles.d) << o.shift) + (i & ((1u << o.shift) - 1u));
-  return x;
-}
-
-constexpr int kRowThreads = 256;
-constexpr int kRowUnroll = 4;
 
 // ---------------------------------------------------------------------------
 // Store.  Eight lanes hold one group of 64 (16 bytes each); minimum and maximum
-// by shuffles.  Consecutive lanes walk rows of one head, so the 16-bit rows are
-// read in segments of K * 2 bytes and the codes are written contiguously.
+// by packed 16-bit comparisons and shuffles.
 // ---------------------------------------------------------------------------
 // c = nearest integer to (x - z) / s, ties to even, decided exactly.  Adding 1.5 2^23
 // to d / s (in one fused step, d = x - z) rounds it to an integer in the low mantissa
@@ -90,59 +79,87 @@ __device__ __noinline__ float code_wide(float x, float z, float s) {
   return static_cast<float>(rint((static_cast<double>(x) - z) / s));
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r =
+        __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r =
+        __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   constexpr int kLanes = D / 8;  // lanes per row
-  constexpr int kRows = kRowThreads / kLanes;
+  const unsigned group =
+      blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;  // of kRowGroup rows
   const int part = threadIdx.x % kLanes;
   const bool value = blockIdx.y != 0;
-  const uint16_t* src = static_cast<const uint16_t*>(value ? a.v_new : a.k_new);
-  const long long sb = value ? a.vn_s[0] : a.kn_s[0], sr = value ? a.vn_s[1] : a.kn_s[1],
-                  sh = value ? a.vn_s[2] : a.kn_s[2];
-  uint32_t* codes = static_cast<uint32_t*>(value ? a.v_codes : a.k_codes);
-  uint32_t* params = static_cast<uint32_t*>(value ? a.v_params : a.k_params);
-  const unsigned first = blockIdx.x * (kRowUnroll * kRows);
-
-  uint4 raw[kRowUnroll];
-  long long dst[kRowUnroll];  // row of the [B, Hkv, cap] planes, or -1
-#pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    const unsigned off = u * kRows + threadIdx.x / kLanes;
-    dst[u] = -1;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (first + off < a.order.total) {
-      const RowAt x = row_at(first + off, a.order);
-      const int n = a.q_lens ? a.q_lens[x.b] : a.M;
-      const int past = a.cache_len[x.b];
-      if (n < 0 || n > a.M || past < 0 || past > a.cap - n) {
-        if (x.r == 0 && x.h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
-      } else if (static_cast<int>(x.r) < n) {
-        dst[u] = (static_cast<long long>(x.b) * a.Hkv + x.h) * a.cap + past + x.r;
-        raw[u] = *reinterpret_cast<const uint4*>(src + x.b * sb + x.r * sr + x.h * sh + part * 8);
-      }
+  const unsigned q = divide(group, a.order.heads), h = group - q * a.order.heads.d;
+  const unsigned b = divide(q, a.order.tiles), r0 = (q - b * a.order.tiles.d) * kRowGroup;
+  int rows = 0;  // of this group
+  long long dst = 0;
+  if (group < a.order.total) {
+    const int n = a.q_lens ? a.q_lens[b] : a.M;
+    const int past = a.cache_len[b];
+    if (n < 0 || n > a.M || past < 0 || past > a.cap - n) {
+      if (r0 == 0 && h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
+    } else {
+      rows = min(n - static_cast<int>(r0), kRowGroup);
+      dst = (static_cast<long long>(b) * a.Hkv + h) * a.cap + past + r0;
     }
   }
+  const long long step = value ? a.vn_s[1] : a.kn_s[1];
+  const uint16_t* src = static_cast<const uint16_t*>(value ? a.v_new : a.k_new) +
+                        b * (value ? a.vn_s[0] : a.kn_s[0]) + r0 * step +
+                        h * (value ? a.vn_s[2] : a.kn_s[2]) + part * 8;
+  uint32_t* codes = static_cast<uint32_t*>(value ? a.v_codes : a.k_codes) + dst * kLanes + part;
+  uint32_t* params =
+      static_cast<uint32_t*>(value ? a.v_params : a.k_params) + dst * (D / 64) + part / 8;
+
+  uint4 raw[kRowGroup];
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
+  for (int u = 0; u < kRowGroup; ++u) {
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (u < rows) raw[u] = *reinterpret_cast<const uint4*>(src + u * step);
+  }
+#pragma unroll
+  for (int u = 0; u < kRowGroup; ++u) {
+    if (__all_sync(0xffffffffu, u >= rows)) break;  // no row left for any lane
     const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-    float x[8];
+    float x[8], bad = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = BF16 ? __uint_as_float(w[i] << 16) : to_f<BF16>(w[i] & 0xffffu);
       x[2 * i + 1] = BF16 ? __uint_as_float(w[i] & 0xffff0000u) : to_f<BF16>(w[i] >> 16);
     }
-    float mn = x[0], mx = x[0], bad = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn = fminf(mn, x[i]);
-      mx = fmaxf(mx, x[i]);
-      bad = fmaf(x[i], 0.f, bad);  // NaN once a value is not finite
-    }
+    for (int i = 0; i < 8; ++i) bad = fmaf(x[i], 0.f, bad);  // NaN once a value is not finite
+    uint32_t lo = min2<BF16>(min2<BF16>(w[0], w[1]), min2<BF16>(w[2], w[3]));
+    uint32_t hi = max2<BF16>(max2<BF16>(w[0], w[1]), max2<BF16>(w[2], w[3]));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      lo = min2<BF16>(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max2<BF16>(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
+    const float mn = fminf(to_f<BF16>(lo & 0xffffu), to_f<BF16>(lo >> 16));
+    const float mx = fmaxf(to_f<BF16>(hi & 0xffffu), to_f<BF16>(hi >> 16));
     const unsigned bad_lanes = __ballot_sync(0xffffffffu, bad != bad);
     const bool bad_group = ((bad_lanes >> (threadIdx.x & 24)) & 0xffu) != 0;
     const float range = mx - mn;  // may pass fp32's largest value for bf16 inputs
@@ -153,7 +170,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     if (bad_group) {
       s16 = z16 = BF16 ? 0x7fc0u : 0x7e00u;  // a group with a NaN or infinity stands for NaN
     } else if (s >= 0x1p-100f && s <= 0x1p100f) {
-      const float inv = 1.f / s;
+      const float inv = __fdividef(1.f, s);  // within 2 ulp, like the 1e-4 next to a half
       float worst = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -176,9 +193,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
       for (int i = 0; i < 8; ++i)
         word |= static_cast<uint32_t>(fminf(fmaxf(code_wide(x[i], z, s), 0.f), 15.f)) << (4 * i);
     }
-    if (dst[u] >= 0) {
-      codes[dst[u] * kLanes + part] = word;
-      if (part % 8 == 0) params[dst[u] * (D / 64) + part / 8] = s16 | (z16 << 16);
+    if (u < rows) {
+      codes[u * kLanes] = word;
+      if (part % 8 == 0) params[u * (D / 64)] = s16 | (z16 << 16);
     }
   }
 }
@@ -200,39 +217,42 @@ __device__ __forceinline__ float fma_16(uint16_t c, uint16_t s, float z) {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs a) {
   constexpr int kLanes = D / 8;
-  constexpr int kRows = kRowThreads / kLanes;
+  const unsigned group =
+      blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;  // of kRowGroup rows
   const int part = threadIdx.x % kLanes;
   const bool value = blockIdx.y != 0;
-  const uint32_t* codes = static_cast<const uint32_t*>(value ? a.v_codes : a.k_codes);
-  const uint32_t* params = static_cast<const uint32_t*>(value ? a.v_params : a.k_params);
-  uint16_t* out = static_cast<uint16_t*>(value ? a.v_out : a.k_out);
-  const long long sb = value ? a.vo_s[0] : a.ko_s[0], sr = value ? a.vo_s[1] : a.ko_s[1],
-                  sh = value ? a.vo_s[2] : a.ko_s[2];
-  const unsigned first = blockIdx.x * (kRowUnroll * kRows);
+  if (group >= a.order.total) return;
+  const unsigned q = divide(group, a.order.heads), h = group - q * a.order.heads.d;
+  const unsigned b = divide(q, a.order.tiles), r0 = (q - b * a.order.tiles.d) * kRowGroup;
+  const int n = a.rows[b];
+  const int skip = a.first ? a.first[b] : 0;
+  if (n < 0 || n > a.out_rows || skip < 0 || skip > a.cap - n) {
+    if (r0 == 0 && h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
+    return;
+  }
+  const int rows = min(n - static_cast<int>(r0), kRowGroup);
+  if (rows <= 0) return;
+  const long long row = (static_cast<long long>(b) * a.Hkv + h) * a.cap + skip + r0;
+  const uint32_t* codes =
+      static_cast<const uint32_t*>(value ? a.v_codes : a.k_codes) + row * kLanes + part;
+  const uint32_t* params =
+      static_cast<const uint32_t*>(value ? a.v_params : a.k_params) + row * (D / 64) + part / 8;
+  const long long step = value ? a.vo_s[1] : a.ko_s[1];
+  uint16_t* out = static_cast<uint16_t*>(value ? a.v_out : a.k_out) +
+                  b * (value ? a.vo_s[0] : a.ko_s[0]) + r0 * step +
+                  h * (value ? a.vo_s[2] : a.ko_s[2]) + part * 8;
 
-  uint32_t word[kRowUnroll], sz[kRowUnroll];
-  long long dst[kRowUnroll];
+  uint32_t word[kRowGroup], sz[kRowGroup];
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    const unsigned off = u * kRows + threadIdx.x / kLanes;
-    dst[u] = -1;
+  for (int u = 0; u < kRowGroup; ++u) {
     word[u] = sz[u] = 0;
-    if (first + off < a.order.total) {
-      const RowAt x = row_at(first + off, a.order);
-      const int n = a.rows[x.b];
-      const int skip = a.first ? a.first[x.b] : 0;
-      if (n < 0 || n > a.out_rows || skip < 0 || skip > a.cap - n) {
-        if (x.r == 0 && x.h == 0 && part == 0) record_error(a.status, kErrInvalidArg);
-      } else if (static_cast<int>(x.r) < n) {
-        const long long row = (static_cast<long long>(x.b) * a.Hkv + x.h) * a.cap + skip + x.r;
-        word[u] = codes[row * kLanes + part];
-        sz[u] = params[row * (D / 64) + part / 8];
-        dst[u] = x.b * sb + x.r * sr + x.h * sh + part * 8;
-      }
+    if (u < rows) {
+      word[u] = codes[u * kLanes];
+      sz[u] = params[u * (D / 64)];
     }
   }
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
+  for (int u = 0; u < kRowGroup; ++u) {
     const uint16_t s = static_cast<uint16_t>(sz[u]);
     const float z = BF16 ? __uint_as_float(sz[u] & 0xffff0000u) : to_f<BF16>(sz[u] >> 16);
     float v[8];
@@ -254,8 +274,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
       v[i] = fma_16<BF16>(static_cast<uint16_t>(c), s, z);
       v[i + 4] = fma_16<BF16>(static_cast<uint16_t>(c >> 16), s, z);
     }
-    if (dst[u] >= 0)
-      *reinterpret_cast<uint4*>(out + dst[u]) =
+    if (u < rows)
+      *reinterpret_cast<uint4*>(out + u * step) =
           make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]),
                      pack2<BF16>(v[6], v[7]));
   }
@@ -836,6 +856,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
   __shared__ float s_lse[256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) < a.merge_blocks) {
     const int row = blockIdx.x * 8 + warp;
     if (row >= a.B * a.Hq) return;
@@ -870,7 +891,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
     if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
     return;
   }
-  // weights
+  // weights: four consecutive rows a thread (score_stride is a multiple of 4)
   const int blk = blockIdx.x - a.merge_blocks;
   const int bh = blk / a.weight_blocks, c0 = (blk - bh * a.weight_blocks) * kWeightRows;
   const int b = bh / a.Hkv, kvh = bh - b * a.Hkv;
@@ -878,34 +899,36 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
   if (n < 0 || n > a.max_len) return;
   const long long wrow = static_cast<long long>(bh) * a.cap;
   const int ns = (n + a.chunk - 1) / a.chunk;
-  const int c1 = min(a.cap, c0 + kWeightRows);
-  float sum[kWeightRows / 256];
-#pragma unroll
-  for (int u = 0; u < kWeightRows / 256; ++u) sum[u] = 0.f;
+  const int j0 = c0 + 4 * threadIdx.x;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const long long row0 = static_cast<long long>(b) * a.Hq + kvh * a.group;
   for (int g0 = 0; g0 < a.group && c0 < n; g0 += 256) {
     const int gn = min(256, a.group - g0);
     __syncthreads();
     for (int g = warp; g < gn; g += 8) {
-      const long long row = static_cast<long long>(b) * a.Hq + kvh * a.group + g0 + g;
-      const float l = merged_lse2(a.part_lse + row * a.max_splits, ns, lane);
+      const float l = merged_lse2(a.part_lse + (row0 + g0 + g) * a.max_splits, ns, lane);
       if (lane == 0) s_lse[g] = l;
     }
     __syncthreads();
-    for (int g = 0; g < gn; ++g) {
-      const float* x = a.scores + (static_cast<long long>(b) * a.Hq + kvh * a.group + g0 + g) *
-                                      a.score_stride;
-      const float l = s_lse[g];
-#pragma unroll
-      for (int u = 0; u < kWeightRows / 256; ++u) {
-        const int j = c0 + u * 256 + threadIdx.x;
-        if (j < n && l != neg_inf()) sum[u] += ex2(x[j] - l);
+    if (j0 < n) {
+      const float* x = a.scores + (row0 + g0) * a.score_stride + j0;
+#pragma unroll 4
+      for (int g = 0; g < gn; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(x + g * a.score_stride);
+        const float l = s_lse[g];
+        if (l != neg_inf()) {
+          sum[0] += ex2(v.x - l);
+          sum[1] += ex2(v.y - l);
+          sum[2] += ex2(v.z - l);
+          sum[3] += ex2(v.w - l);
+        }
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < kWeightRows / 256; ++u) {
-    const int j = c0 + u * 256 + threadIdx.x;
-    if (j < c1)
+  for (int u = 0; u < 4; ++u) {
+    const int j = j0 + u;
+    if (j < min(a.cap, c0 + kWeightRows))
       a.w_out[wrow + j] = j < n ? sum[u] + (a.w_in ? a.w_in[wrow + j] : 0.f) : 0.f;
   }
 }
@@ -928,18 +951,19 @@ cudaError_t decode_t(const Kv4DecodeArgs& a, bool alibi, cudaStream_t stream) {
   const long long blocks =
       a.merge_blocks + static_cast<long long>(a.B) * a.Hkv * a.weight_blocks;
   if (blocks == 0) return cudaSuccess;
-  kv4_merge_kernel<D, BF16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kv4_merge_kernel<D, BF16>, dim3(static_cast<unsigned>(blocks)), 256, 0,
+                      stream, a);
 }
 
 }  // namespace
 
 int kv4_weight_rows() { return kWeightRows; }
+int kv4_row_group() { return kRowGroup; }
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, bool bf16,
                               cudaStream_t stream) {
-  const long long per = static_cast<long long>(kRowUnroll) * kRowThreads * 8 / head_dim;
-  const dim3 grid(static_cast<unsigned>((a.order.total + per - 1) / per), 2);
+  const unsigned per = kRowThreads * 8 / head_dim;  // row groups a block
+  const dim3 grid((a.order.total + per - 1) / per, 2);
   if (head_dim == 64 && !bf16) kv4_append_kernel<64, false><<<grid, kRowThreads, 0, stream>>>(a);
   else if (head_dim == 64) kv4_append_kernel<64, true><<<grid, kRowThreads, 0, stream>>>(a);
   else if (!bf16) kv4_append_kernel<128, false><<<grid, kRowThreads, 0, stream>>>(a);
@@ -948,8 +972,8 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, bool bf16,
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int head_dim, bool bf16, cudaStream_t stream) {
-  const long long per = static_cast<long long>(kRowUnroll) * kRowThreads * 8 / head_dim;
-  const dim3 grid(static_cast<unsigned>((a.order.total + per - 1) / per), 2);
+  const unsigned per = kRowThreads * 8 / head_dim;  // row groups a block
+  const dim3 grid((a.order.total + per - 1) / per, 2);
   if (head_dim == 64 && !bf16) kv4_read_kernel<64, false><<<grid, kRowThreads, 0, stream>>>(a);
   else if (head_dim == 64) kv4_read_kernel<64, true><<<grid, kRowThreads, 0, stream>>>(a);
   else if (!bf16) kv4_read_kernel<128, false><<<grid, kRowThreads, 0, stream>>>(a);
