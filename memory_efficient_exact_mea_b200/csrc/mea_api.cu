@@ -116,21 +116,8 @@ namespace mea {
 int* device_status_word() { return status_word(); }
 
 bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int batch, int rows, int heads,
-                 int K, const int64_t st[3], int box_heads, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(heads),
-                              static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]) * 2,
-                                 static_cast<cuuint64_t>(st[1]) * 2,
-                                 static_cast<cuuint64_t>(st[0]) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads),
-                             static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                 int K, const int64_t st[3], int box_rows) {
+  return encode_bmhk(map, base, bf16, batch, rows, heads, K, st, box_rows);
 }
 
 }  // namespace mea

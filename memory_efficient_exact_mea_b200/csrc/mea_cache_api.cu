@@ -8,12 +8,6 @@
 #include "mea.h"
 #include "mea_internal.h"
 
-#ifndef MEA_CHUNK
-#define MEA_CHUNK 1024
-#endif
-#ifndef MEA_FILL
-#define MEA_FILL 6
-#endif
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -38,6 +32,10 @@ bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
   return true;
 }
 
+// mea_key_weights with at most this many query rows and (row, query head) pairs a kv
+// head goes to the kernel that reads K once with mma.sync.
+constexpr int kFewRows = 16, kFewColumns = 128;
+
 // Splits of one decode call.  A split is a whole number of 128-row steps (four
 // warps of 32 rows); long enough that its partial state (K floats a head) and
 // its start-up stay small beside the rows it reads, short enough that the grid
@@ -50,9 +48,9 @@ DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
   DecodePlan p{};
   p.head_blocks = (Hq / Hkv + 7) / 8;
   const int64_t units = static_cast<int64_t>(B) * Hkv * p.head_blocks;
-  const int64_t want = std::max<int64_t>(1, 148 * MEA_FILL / std::max<int64_t>(1, units));
+  const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
   int64_t chunk = (max_len + want - 1) / want;
-  chunk = std::min<int64_t>(MEA_CHUNK, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  chunk = std::min<int64_t>(2048, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);
   return p;
@@ -256,19 +254,24 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
   a.status = mea::device_status_word();
   if (!a.status) return MEA_ERR_CUDA;
   a.group = Hq / Hkv;
-  // Few rows: the group's heads share one 16-column tile.
-  L.narrow = M <= 16;
-  a.box_heads = 1;
-  a.box_rows = 128;
-  if (L.narrow) {
-    while (a.box_heads < a.group && a.box_heads < 16) a.box_heads *= 2;
-    a.box_rows = 16 / a.box_heads;
-    while ((1 << a.box_shift) < a.box_heads) ++a.box_shift;
-  }
+  // Few (row, head) pairs to a key: the kernel that is bound by reading K.
+  L.few = M <= kFewRows && static_cast<int64_t>(M) * a.group <= kFewColumns && Hkv <= 65535 &&
+          B <= 65535;
   const bool bf16 = dtype == MEA_BF16;
-  if (!mea::encode_rows(&L.tmQ, q, bf16, B, M, Hq, K, q_strides, a.box_heads, a.box_rows) ||
-      !mea::encode_rows(&L.tmK, k, bf16, B, N, Hkv, K, k_strides, 1, mea::kWeightKeys))
+  if (L.few) {
+    const int64_t units = static_cast<int64_t>(B) * Hkv;
+    const int64_t chunk = (units * N / (148 * 8) + 63) / 64 * 64;
+    a.few_chunk = static_cast<int>(std::min<int64_t>(512, std::max<int64_t>(64, chunk)));
+    for (int i = 0; i < 3; ++i) {
+      a.q_s[i] = q_strides[i];
+      a.k_s[i] = k_strides[i];
+    }
+    L.q = q;
+    L.k = k;
+  } else if (!mea::encode_rows(&L.tmQ, q, bf16, B, M, Hq, K, q_strides, 128) ||
+             !mea::encode_rows(&L.tmK, k, bf16, B, N, Hkv, K, k_strides, mea::kWeightKeys)) {
     return MEA_ERR_CUDA;
+  }
   a.lse = lse;
   a.w_in = weights_in;
   a.w_out = weights_out;

@@ -162,9 +162,9 @@ int bwd_dq_box_rows(int head_dim);  // rows of the dq accumulator's TMA reductio
 int* device_status_word();  // nullptr if the lookup fails
 
 // A [batch, rows, heads, K] 16-bit tensor with element strides st = {b, row,
-// head} as a rank-4 TMA map with boxes of 64 elements x box_heads x box_rows.
+// head} as a rank-4 TMA map with boxes of 64 elements x 1 head x box_rows.
 bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int batch, int rows, int heads,
-                 int K, const int64_t st[3], int box_heads, int box_rows);
+                 int K, const int64_t st[3], int box_rows);
 
 // ---------------------------------------------------------------------------
 // 4-bit cache (mea_kv4_sm100.cu): planes [B, Hkv, cap, ...], contiguous.
@@ -239,7 +239,7 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, bool bf16, b
 // ---------------------------------------------------------------------------
 // Gathered key weights (mea_weights_sm100.cu).
 // ---------------------------------------------------------------------------
-constexpr int kWeightKeys = 128;  // keys per CTA
+constexpr int kWeightKeys = 128;  // keys per A operand
 
 struct WeightArgs {
   const float* lse;          // [B, Hq, M]
@@ -249,17 +249,18 @@ struct WeightArgs {
   const int32_t* q_lens;     // [B] or nullptr: M
   int* status;
   int B, M, N, Hq, Hkv, group;
-  int box_heads, box_rows;   // query tile: box_heads (a power of two) heads x box_rows rows
-  int box_shift;             // log2(box_heads)
   float scale_log2;
+  int few_chunk;             // few rows only: keys per CTA (a multiple of 64)
+  long long q_s[3], k_s[3];  // few rows only: element strides (b, row, head)
 };
 
 struct WeightLaunch {
   CUtensorMap tmQ, tmK;
+  const void *q, *k;
   WeightArgs args;
   int head_dim;
   bool bf16, causal, alibi;
-  bool narrow;  // 16-column query tiles
+  bool few;  // few query rows: K read once, mma.sync
 };
 
 cudaError_t launch_weights(const WeightLaunch& launch, cudaStream_t stream);

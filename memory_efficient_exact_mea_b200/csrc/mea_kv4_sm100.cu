@@ -308,9 +308,6 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // rows' words.  Each warp copies its own tiles into a ring of its own (cp.async,
 // 16-byte chunks, no barrier but __syncwarp), two tiles ahead.
 // ---------------------------------------------------------------------------
-#ifndef MEA_OCC
-#define MEA_OCC 4
-#endif
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;        // rows per warp and iteration
@@ -422,7 +419,7 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 }
 
 template <int D, bool BF16, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, MEA_OCC) kv4_decode_kernel(const Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = KSmem<D>;
   constexpr int NG = L::NG;  // groups of a row
   extern __shared__ __align__(128) uint8_t smem[];
@@ -900,36 +897,47 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
   const long long wrow = static_cast<long long>(bh) * a.cap;
   const int ns = (n + a.chunk - 1) / a.chunk;
   const int j0 = c0 + 4 * threadIdx.x;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  float sum[4] = {0.f, 0.f, 0.f, 0.f}, w_in[4] = {0.f, 0.f, 0.f, 0.f};
   const long long row0 = static_cast<long long>(b) * a.Hq + kvh * a.group;
+  if (a.w_in != nullptr) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j0 + u < n) w_in[u] = a.w_in[wrow + j0 + u];
+  }
+  constexpr int kAhead = 4;  // heads whose scores are fetched before their lse is joined
   for (int g0 = 0; g0 < a.group && c0 < n; g0 += 256) {
     const int gn = min(256, a.group - g0);
+    const float* x = a.scores + (row0 + g0) * a.score_stride + j0;
+    float4 v[kAhead];
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g)
+      v[g] = g < gn && j0 < n ? *reinterpret_cast<const float4*>(x + g * a.score_stride)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
     for (int g = warp; g < gn; g += 8) {
       const float l = merged_lse2(a.part_lse + (row0 + g0 + g) * a.max_splits, ns, lane);
       if (lane == 0) s_lse[g] = l;
     }
     __syncthreads();
-    if (j0 < n) {
-      const float* x = a.scores + (row0 + g0) * a.score_stride + j0;
-#pragma unroll 4
-      for (int g = 0; g < gn; ++g) {
-        const float4 v = *reinterpret_cast<const float4*>(x + g * a.score_stride);
-        const float l = s_lse[g];
-        if (l != neg_inf()) {
-          sum[0] += ex2(v.x - l);
-          sum[1] += ex2(v.y - l);
-          sum[2] += ex2(v.z - l);
-          sum[3] += ex2(v.w - l);
-        }
-      }
-    }
+    auto add = [&](const float4& y, float l) {
+      if (l == neg_inf()) return;
+      sum[0] += ex2(y.x - l);
+      sum[1] += ex2(y.y - l);
+      sum[2] += ex2(y.z - l);
+      sum[3] += ex2(y.w - l);
+    };
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g)
+      if (g < gn) add(v[g], s_lse[g]);
+    if (j0 < n)
+      for (int g = kAhead; g < gn; ++g)
+        add(*reinterpret_cast<const float4*>(x + g * a.score_stride), s_lse[g]);
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int j = j0 + u;
     if (j < min(a.cap, c0 + kWeightRows))
-      a.w_out[wrow + j] = j < n ? sum[u] + (a.w_in ? a.w_in[wrow + j] : 0.f) : 0.f;
+      a.w_out[wrow + j] = j < n ? sum[u] + w_in[u] : 0.f;
   }
 }
 

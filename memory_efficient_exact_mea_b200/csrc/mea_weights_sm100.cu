@@ -11,11 +11,10 @@
 // thread's own row -- no reduction across lanes, no atomics, the same order every
 // time.  For each 128 keys, two groups of four warps take alternate tiles (one TMEM
 // buffer each), so one group's exponentials overlap the other's MMA and TMEM read.  Bound by
-// the exponential unit (16 a clock per SM) for long query blocks, by reading K
-// for a single query row.
+// the exponential unit (16 a clock per SM).
 //
-// Query tiles: 128 rows of one head; or 16 columns of box_heads heads x box_rows
-// rows when there are few rows (a decode step's group of heads shares one tile).
+// A few query rows (a decode step, a short chunk) go to weights_few_kernel: the same
+// sum with mma.sync straight from global memory, bound by reading K once.
 #include <math.h>
 
 #include <type_traits>
@@ -29,19 +28,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-
-// 32 lanes x 16 columns (thread t: lane quarter + t) and the wait for them.
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 
 // acc + 2^x for a pair, on the FMA pipe: 2^x = 2^n 2^f with n the integer next to x
 // (added into the low mantissa bits of 1.5 2^23) and 2^f, |f| <= 1/2, by a polynomial
@@ -70,31 +56,32 @@ __device__ __forceinline__ f2 exp2_add(f2 x, f2 acc) {
   return fma2(p, two_n, acc);
 }
 
-#ifndef MEA_POLY_OF_16
-#define MEA_POLY_OF_16 6
-#endif
-// Which of a chunk's 16 pairs take the polynomial, spread evenly.
+// Which of a chunk's 16 pairs take the polynomial, spread evenly: the exponential
+// unit alone measured 372 / 178 us (causal 4 x 4096, two-sided 8 x 2048), 3 of 16
+// pairs here 349 / 164 us, 5 of 16 358 / 167 us.
+constexpr int kPolyOf16 = 3;
 __device__ __forceinline__ constexpr bool on_fma_pipe(int pair) {
-  return (pair * MEA_POLY_OF_16) % 16 < MEA_POLY_OF_16;
+  return (pair * kPolyOf16) % 16 < kPolyOf16;
 }
 
-// NQ = 128: a query tile is used against kHalves x 128 keys, 2 halves at K = 128 (one
+// A query tile is used against kHalves x 128 keys, 2 halves at K = 128 (one
 // CTA per SM), 1 at K = 64 (two CTAs): 1 byte of Q read from L2 per score either way.
 // Query tiles are released as soon as their MMAs have read them, so the ring runs
 // four or five tiles ahead; lse has a ring of its own that lives until the tile's
 // sums are done.
-template <int D, int NQ>
+template <int D>
 struct WCfg {
-  static constexpr int kHalves = (NQ == 128 && D == 128) ? 2 : 1;
+  static constexpr int NQ = 128;  // query rows per tile
+  static constexpr int kHalves = D == 128 ? 2 : 1;
   static constexpr int kKeys = kHalves * kWeightKeys;
-  static constexpr int kParity = NQ == 16 ? 1 : 2;  // consumer groups per half
+  static constexpr int kParity = 2;  // consumer groups per half
   static constexpr int kGroups = kHalves * kParity;  // of four warps
   static constexpr int kWarps = 4 * kGroups;
   static constexpr int kThreads = (kWarps + 2) * 32;
   static constexpr int kMmaWarp = kWarps, kLoadWarp = kWarps + 1;
-  static constexpr int kStages = NQ == 16 ? 2 : (D == 128 ? 4 : 5);
+  static constexpr int kStages = D == 128 ? 4 : 5;
   static constexpr int kLseSlots = 8;
-  static constexpr int kCtas = NQ == 16 ? 4 : (kHalves == 2 ? 1 : 2);  // per SM
+  static constexpr int kCtas = kHalves == 2 ? 1 : 2;  // per SM
   static constexpr int kChunks = D / 64;
   static constexpr int kKChunk = kWeightKeys * 128;
   static constexpr int kQChunk = NQ * 128;
@@ -102,8 +89,8 @@ struct WCfg {
   static constexpr int kQTile = kChunks * kQChunk;
   static constexpr int kQ = kHalves * kKTile;
   static constexpr int kLse = kQ + kStages * kQTile;      // [slot][NQ] -lse * log2(e)
-  static constexpr int kSlope = kLse + kLseSlots * NQ * 4;  // [slot][NQ] (narrow), [slot] (wide)
-  static constexpr int kSum = kSlope + kLseSlots * (NQ == 16 ? 16 : 1) * 4;  // [kKeys]
+  static constexpr int kSlope = kLse + kLseSlots * NQ * 4;  // [slot] the tile's ALiBi slope
+  static constexpr int kSum = kSlope + kLseSlots * 4;      // [kKeys]
   static constexpr int kBar = kSum + kKeys * 4;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kLseSlots + 4 * kHalves;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
@@ -113,11 +100,12 @@ struct WCfg {
   static constexpr uint32_t kTmemCols = 2 * kHalves * NQ;  // two buffers a half
 };
 
-template <int D, bool BF16, int NQ, bool CAUSAL, bool ALIBI>
-__global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
+template <int D, bool BF16, bool CAUSAL, bool ALIBI>
+__global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
     weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const WeightArgs a) {
-  using C = WCfg<D, NQ>;
+  using C = WCfg<D>;
+  constexpr int NQ = C::NQ;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -154,13 +142,11 @@ __global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
   }
   // without cache_len the N keys are all there, whatever m is
   const int n = a.cache_len ? past + m : a.N;
-  // (head block, row block) pairs; a causal key block starts at the first row that sees it
-  const int rows = NQ == 16 ? a.box_rows : NQ;
-  const int hblocks = (a.group + a.box_heads - 1) / a.box_heads;
+  // (head, row block) pairs; a causal key block starts at the first row that sees it
   int m_first = 0;
-  if constexpr (CAUSAL) m_first = max(0, n0 - past) / rows * rows;
-  const int mblocks = m > m_first ? (m - m_first + rows - 1) / rows : 0;
-  const int steps = n0 < n ? hblocks * mblocks : 0;
+  if constexpr (CAUSAL) m_first = max(0, n0 - past) / NQ * NQ;
+  const int mblocks = m > m_first ? (m - m_first + NQ - 1) / NQ : 0;
+  const int steps = n0 < n ? a.group * mblocks : 0;
   if (steps == 0) {  // no query sees these keys
     if (threadIdx.x < C::kKeys && n0 + static_cast<int>(threadIdx.x) < a.N) {
       const int j = n0 + threadIdx.x;
@@ -207,40 +193,29 @@ __global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
     }
     int issued = 0;
     for (int s = 0; s < steps; ++s) {
-      const int hb = s / mblocks, m0 = m_first + (s - hb * mblocks) * rows;
+      const int g = s / mblocks, m0 = m_first + (s - g * mblocks) * NQ;
       const int slot = s % C::kStages, ls = s % C::kLseSlots;
-      float l2[(NQ + 31) / 32], sl[(NQ + 31) / 32];
+      const int h = kvh * a.group + g;
+      float l2[NQ / 32];
 #pragma unroll
-      for (int u = 0; u < (NQ + 31) / 32; ++u) {  // in flight during the waits
-        const int c = u * 32 + lane;
-        const int g = hb * a.box_heads + (NQ == 16 ? c & (a.box_heads - 1) : 0);
-        const int i = m0 + (NQ == 16 ? c >> a.box_shift : c);
-        l2[u] = neg_inf();
-        sl[u] = 0.f;
-        if (c < NQ && i < m && g < a.group) {
-          const int h = kvh * a.group + g;
-          l2[u] = a.lse[(static_cast<long long>(b) * a.Hq + h) * a.M + i];
-          if constexpr (ALIBI) sl[u] = exp2f(-8.0f * static_cast<float>(h + 1) / a.Hq) * kLog2e;
-        }
+      for (int u = 0; u < NQ / 32; ++u) {  // in flight during the waits
+        const int i = m0 + u * 32 + lane;
+        l2[u] = i < m ? a.lse[(static_cast<long long>(b) * a.Hq + h) * a.M + i] : neg_inf();
       }
       if (!mbar_wait_warp(&q_empty[slot], ((s / C::kStages) & 1) ^ 1, abort_flag, a.status)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&q_full[slot], C::kQTile);
         for (int c = 0; c < C::kChunks; ++c)
           tma_load_4d(smem + C::kQ + slot * C::kQTile + c * C::kQChunk, &tmQ, &q_full[slot],
-                      c * 64, kvh * a.group + hb * a.box_heads, m0, b);
+                      c * 64, h, m0, b);
       }
       ++issued;
       if (!mbar_wait_warp(&l_empty[ls], ((s / C::kLseSlots) & 1) ^ 1, abort_flag, a.status)) break;
 #pragma unroll
-      for (int u = 0; u < (NQ + 31) / 32; ++u) {
-        const int c = u * 32 + lane;
-        if (c < NQ) {  // -inf: the row takes no weight
-          s_lse[ls * NQ + c] = l2[u] == neg_inf() ? l2[u] : -l2[u] * kLog2e;
-          if (ALIBI && NQ == 16) s_slope[ls * NQ + c] = sl[u];
-          if (ALIBI && NQ == 128 && c == 0) s_slope[ls] = sl[u];
-        }
-      }
+      for (int u = 0; u < NQ / 32; ++u)  // -inf: the row takes no weight
+        s_lse[ls * NQ + u * 32 + lane] = l2[u] == neg_inf() ? l2[u] : -l2[u] * kLog2e;
+      if (ALIBI && lane == 0)
+        s_slope[ls] = exp2f(-8.0f * static_cast<float>(h + 1) / a.Hq) * kLog2e;
       mbar_arrive_warp(&l_full[ls]);
     }
     if (lane == 0) {  // no copy may be in flight when the CTA ends
@@ -284,48 +259,38 @@ __global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
     f2 acc = {0.f, 0.f};
     const f2 sc2 = {a.scale_log2, a.scale_log2};
     for (int s = grp % C::kParity; s < steps; s += C::kParity) {
-      const int hb = s / mblocks, m0 = m_first + (s - hb * mblocks) * rows;
+      const int g = s / mblocks, m0 = m_first + (s - g * mblocks) * NQ;
       const int ls = s % C::kLseSlots, buf = 2 * half + (s & 1);
       // row i = m0 + row(c) sees this key iff i >= key - past
       const int first = CAUSAL ? max(0, key - past - m0) : 0;
-      const bool whole = NQ == 128 && m0 + NQ <= m &&
+      const bool whole = m0 + NQ <= m &&
                          (!CAUSAL || n0 + (half + 1) * kWeightKeys - 1 - past <= m0);
       if (!mbar_wait_warp(&l_full[ls], (s / C::kLseSlots) & 1, abort_flag, a.status) ||
           !mbar_wait_warp(&s_full[buf], (s >> 1) & 1, abort_flag, a.status))
         break;
       tc_fence_after();
       const float* lse = s_lse + ls * NQ;
-      const float slope = ALIBI && NQ == 128 ? s_slope[ls] : 0.f;
+      [[maybe_unused]] const float slope = ALIBI ? s_slope[ls] : 0.f;
       // `open`: every column of the tile counts for every key of it
       auto add_tile = [&](auto open) {
 #pragma unroll 1
         for (int c0 = 0; c0 < NQ; c0 += 32) {
           uint32_t r[32];
-          if constexpr (NQ == 16) {
-            tmem_ld16_wait(tmem_base + buf * NQ + lane_addr, r);
-          } else {
-            tmem_ld32(tmem_base + buf * NQ + c0 + lane_addr, r);
-            tmem_ld_wait(r);
-          }
+          tmem_ld32(tmem_base + buf * NQ + c0 + lane_addr, r);
+          tmem_ld_wait(r);
           if (c0 + 32 >= NQ) {
             tc_fence_before();
             mbar_arrive_warp(&s_free[buf]);
           }
           [[maybe_unused]] const float dist =
-              ALIBI ? static_cast<float>(past + m0 + (NQ == 16 ? 0 : c0) - key) : 0.f;
+              ALIBI ? static_cast<float>(past + m0 + c0 - key) : 0.f;
 #pragma unroll
-          for (int c = 0; c < (NQ == 16 ? 16 : 32); c += 2) {
+          for (int c = 0; c < 32; c += 2) {
             const f2 nl = *reinterpret_cast<const f2*>(lse + c0 + c);
             f2 x = fma2({__uint_as_float(r[c]), __uint_as_float(r[c + 1])}, sc2, nl);
-            const int r0 = NQ == 16 ? c >> a.box_shift : c0 + c;
-            const int r1 = NQ == 16 ? (c + 1) >> a.box_shift : c0 + c + 1;
             if constexpr (ALIBI) {
-              const float sl0 = NQ == 16 ? s_slope[ls * NQ + c] : slope;
-              const float sl1 = NQ == 16 ? s_slope[ls * NQ + c + 1] : slope;
-              const float d0 = NQ == 16 ? dist + r0 : dist + c,
-                          d1 = NQ == 16 ? dist + r1 : d0 + 1.f;
-              x.x = fmaf(-sl0, fabsf(d0), x.x);
-              x.y = fmaf(-sl1, fabsf(d1), x.y);
+              x.x = fmaf(-slope, fabsf(dist + c), x.x);
+              x.y = fmaf(-slope, fabsf(dist + (c + 1)), x.y);
             }
             if constexpr (open) {
               if (on_fma_pipe(c / 2)) {
@@ -335,8 +300,8 @@ __global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
               }
             } else {
               f2 e = {ex2(x.x), ex2(x.y)};
-              if (nl.x == neg_inf() || r0 < first) e.x = 0.f;
-              if (nl.y == neg_inf() || r1 < first) e.y = 0.f;
+              if (nl.x == neg_inf() || c0 + c < first) e.x = 0.f;
+              if (nl.y == neg_inf() || c0 + c + 1 < first) e.y = 0.f;
               acc = add2(acc, e);
             }
           }
@@ -361,38 +326,184 @@ __global__ void __launch_bounds__(WCfg<D, NQ>::kThreads, WCfg<D, NQ>::kCtas)
   }
 }
 
-template <int D, bool BF16, int NQ, bool CAUSAL, bool ALIBI>
-cudaError_t launch_t(const WeightLaunch& L, cudaStream_t stream) {
-  constexpr auto kern = weights_kernel<D, BF16, NQ, CAUSAL, ALIBI>;
-  constexpr int smem = WCfg<D, NQ>::kBytes;
-  const cudaError_t e = set_smem_once<kern>(smem);
-  if (e != cudaSuccess) return e;
-  const WeightArgs& a = L.args;
-  constexpr int keys = WCfg<D, NQ>::kKeys;
-  const long long blocks = static_cast<long long>((a.N + keys - 1) / keys) * a.Hkv * a.B;
-  kern<<<static_cast<unsigned>(blocks), WCfg<D, NQ>::kThreads, smem, stream>>>(L.tmQ, L.tmK, a);
-  return cudaGetLastError();
+// ---------------------------------------------------------------------------
+// Few query rows: the (row, head) pairs of a kv head's group are the columns of
+// S^T = K Q^T, 8 to a product; a warp takes 16 keys at a time straight from global
+// memory into the A fragment (16 bytes of a row a thread and load: the order of the
+// contraction index is free, so a thread's 8 consecutive dimensions are two of its
+// operand pairs in two steps), the next 16 in flight; Q and lse wait in shared
+// memory in fragment order.  Bound by reading K.
+// ---------------------------------------------------------------------------
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = kFewWarps * 32;
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, bool BF16, int NQ>
-cudaError_t launch_m(const WeightLaunch& L, cudaStream_t stream) {
-  if (L.causal) return L.alibi ? launch_t<D, BF16, NQ, true, true>(L, stream)
-                               : launch_t<D, BF16, NQ, true, false>(L, stream);
-  return L.alibi ? launch_t<D, BF16, NQ, false, true>(L, stream)
-                 : launch_t<D, BF16, NQ, false, false>(L, stream);
+struct FewColumn {  // of one (row, head) pair
+  float nl;     // -lse log2(e); -inf: takes no weight
+  float slope;  // ALiBi, log2 units
+  int pos;      // position of the row
+  int last;     // last key it sees
+};
+
+template <int D, bool BF16, bool ALIBI>
+__global__ void __launch_bounds__(kFewThreads, 4)
+    weights_few_kernel(const WeightArgs a, const uint16_t* q, const uint16_t* k, bool causal,
+                       int blocks) {
+  constexpr int J = D / 32;  // 16-byte loads of a row a thread
+  extern __shared__ __align__(16) uint8_t smem[];
+  FewColumn* s_col = reinterpret_cast<FewColumn*>(smem);               // [blocks * 8]
+  uint4* s_q = reinterpret_cast<uint4*>(smem + blocks * 8 * sizeof(FewColumn));  // [blocks][J][32]
+  const int kvh = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int m = a.q_lens ? a.q_lens[b] : a.M;
+  const int past = a.cache_len ? a.cache_len[b] : a.N - a.M;
+  if (m < 0 || m > a.M || (a.cache_len && past < 0) || past > a.N - m) {
+    if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) record_error(a.status, kErrInvalidArg);
+    return;
+  }
+  const int n = a.cache_len ? past + m : a.N;
+  const int c0 = blockIdx.x * a.few_chunk, c1 = min(a.N, c0 + a.few_chunk);
+  const int k1 = min(c1, n);  // keys [c0, k1) are there
+  float* w_out = a.w_out + (static_cast<long long>(b) * a.Hkv + kvh) * a.N;
+  const float* w_in = a.w_in ? a.w_in + (static_cast<long long>(b) * a.Hkv + kvh) * a.N : nullptr;
+  for (int j = max(c0, n) + threadIdx.x; j < c1; j += kFewThreads) w_out[j] = 0.f;
+  if (c0 >= k1) return;
+
+  const uint16_t* kb = k + b * a.k_s[0] + kvh * a.k_s[2] + 8 * tig;
+  auto fetch = [&](int t, uint4(&r)[2][J]) {  // rows gid, gid + 8; past the end the last again
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4* row = reinterpret_cast<const uint4*>(
+          kb + static_cast<long long>(min(t + gid + 8 * h, k1 - 1)) * a.k_s[1]);
+#pragma unroll
+      for (int j = 0; j < J; ++j) r[h][j] = __ldg(row + 4 * j);
+    }
+  };
+  int t = c0 + warp * 16;
+  uint4 cur[2][J];
+  if (t < k1) fetch(t, cur);
+
+  const int cols = a.M * a.group;
+  for (int c = threadIdx.x; c < blocks * 8; c += kFewThreads) {
+    const int i = c / a.group, h = kvh * a.group + c % a.group;
+    FewColumn x{neg_inf(), 0.f, 0, 0x7fffffff};
+    if (c < cols && i < m) {
+      const float l = a.lse[(static_cast<long long>(b) * a.Hq + h) * a.M + i];
+      if (l != neg_inf()) x.nl = -l * kLog2e;
+      x.slope = exp2f(-8.0f * static_cast<float>(h + 1) / a.Hq) * kLog2e;
+      x.pos = past + i;
+      if (causal) x.last = past + i;
+    }
+    s_col[c] = x;
+  }
+  for (int e = threadIdx.x; e < blocks * J * 32; e += kFewThreads) {
+    const int l = e & 31, j = (e >> 5) % J, c = (e >> 5) / J * 8 + (l >> 2);
+    const int i = c / a.group, h = kvh * a.group + c % a.group;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (c < cols && i < m)
+      x = __ldg(reinterpret_cast<const uint4*>(q + b * a.q_s[0] + i * a.q_s[1] + h * a.q_s[2] +
+                                               32 * j + 8 * (l & 3)));
+    s_q[e] = x;
+  }
+  __syncthreads();
+
+  for (; t < k1; t += kFewWarps * 16) {
+    uint4 nxt[2][J];
+    if (t + kFewWarps * 16 < k1) fetch(t + kFewWarps * 16, nxt);
+    float sum[2] = {0.f, 0.f};
+    for (int blk = 0; blk < blocks; ++blk) {
+      float sc[2][4];  // two chains, half of the dimensions each
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint4 x = s_q[(blk * J + j) * 32 + lane];
+        mma16816<BF16>(sc[0], cur[0][j].x, cur[1][j].x, cur[0][j].y, cur[1][j].y, x.x, x.y);
+        mma16816<BF16>(sc[1], cur[0][j].z, cur[1][j].z, cur[0][j].w, cur[1][j].w, x.z, x.w);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const FewColumn c = s_col[blk * 8 + 2 * tig + e];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = t + gid + 8 * h;
+          float x = fmaf(sc[0][2 * h + e] + sc[1][2 * h + e], a.scale_log2, c.nl);
+          if constexpr (ALIBI) x = fmaf(-c.slope, fabsf(static_cast<float>(c.pos - key)), x);
+          sum[h] += (c.nl == neg_inf() || key > c.last) ? 0.f : ex2(x);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+      const int key = t + gid + 8 * h;
+      if (tig == 0 && key < k1) w_out[key] = sum[h] + (w_in ? w_in[key] : 0.f);
+#pragma unroll
+      for (int j = 0; j < J; ++j) cur[h][j] = nxt[h][j];
+    }
+  }
 }
 
 template <int D, bool BF16>
-cudaError_t launch_n(const WeightLaunch& L, cudaStream_t stream) {
-  return L.narrow ? launch_m<D, BF16, 16>(L, stream) : launch_m<D, BF16, 128>(L, stream);
+cudaError_t launch_few(const WeightLaunch& L, cudaStream_t stream) {
+  const WeightArgs& a = L.args;
+  const int blocks = (a.M * a.group + 7) / 8;
+  const int smem = blocks * (8 * static_cast<int>(sizeof(FewColumn)) + D / 32 * 32 * 16);
+  const dim3 grid((a.N + a.few_chunk - 1) / a.few_chunk, a.Hkv, a.B);
+  const uint16_t* q = static_cast<const uint16_t*>(L.q);
+  const uint16_t* k = static_cast<const uint16_t*>(L.k);
+  if (L.alibi)
+    weights_few_kernel<D, BF16, true><<<grid, kFewThreads, smem, stream>>>(a, q, k, L.causal, blocks);
+  else
+    weights_few_kernel<D, BF16, false><<<grid, kFewThreads, smem, stream>>>(a, q, k, L.causal, blocks);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16, bool CAUSAL, bool ALIBI>
+cudaError_t launch_t(const WeightLaunch& L, cudaStream_t stream) {
+  constexpr auto kern = weights_kernel<D, BF16, CAUSAL, ALIBI>;
+  constexpr int smem = WCfg<D>::kBytes, keys = WCfg<D>::kKeys;
+  const cudaError_t e = set_smem_once<kern>(smem);
+  if (e != cudaSuccess) return e;
+  const WeightArgs& a = L.args;
+  const long long blocks = static_cast<long long>((a.N + keys - 1) / keys) * a.Hkv * a.B;
+  kern<<<static_cast<unsigned>(blocks), WCfg<D>::kThreads, smem, stream>>>(L.tmQ, L.tmK, a);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_d(const WeightLaunch& L, cudaStream_t stream) {
+  if (L.few) return launch_few<D, BF16>(L, stream);
+  if (L.causal) return L.alibi ? launch_t<D, BF16, true, true>(L, stream)
+                               : launch_t<D, BF16, true, false>(L, stream);
+  return L.alibi ? launch_t<D, BF16, false, true>(L, stream)
+                 : launch_t<D, BF16, false, false>(L, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_weights(const WeightLaunch& L, cudaStream_t stream) {
   if (L.head_dim == 64)
-    return L.bf16 ? launch_n<64, true>(L, stream) : launch_n<64, false>(L, stream);
-  return L.bf16 ? launch_n<128, true>(L, stream) : launch_n<128, false>(L, stream);
+    return L.bf16 ? launch_d<64, true>(L, stream) : launch_d<64, false>(L, stream);
+  return L.bf16 ? launch_d<128, true>(L, stream) : launch_d<128, false>(L, stream);
 }
 
 }  // namespace mea
