@@ -431,46 +431,57 @@ def mea_decode(q, k_cache, v_cache, kv_seqstart, max_kv_len: int, scale: float |
     return out, lse
 
 
-def _launch(name, fn, device, stream, scratch, args):
-    """Runs fn(*args, stream) with `device` current.  `scratch` are the tensors this
-    call allocated: on a stream that is not the one they were allocated for, their
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(name, fn, index, stream, scratch, args):
+    """Runs fn(*args, stream) with CUDA device `index` current.  `scratch` are the tensors
+    this call allocated: on a stream that is not the one they were allocated for, their
     memory may not be handed out again before the call has run."""
-    other = device.index is not None and device.index != torch.cuda.current_device()
-    with torch.cuda.device(device) if other else _NO_GUARD:
-        if stream is not None:
-            for t in scratch:
-                if t is not None:
-                    t.record_stream(stream)
-        rc = fn(*args, _stream(stream, device))
-    _check(name, rc)
+    if stream is None:
+        raw = _raw_stream(index) if _raw_stream is not None else \
+            torch.cuda.current_stream(index).cuda_stream
+    else:
+        raw = stream.cuda_stream
+        for t in scratch:
+            t.record_stream(stream)
+    if index == _current_device():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise MeaError(name, rc)
 
 
-class _NoGuard:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
-_NO_GUARD = _NoGuard()
+def _cuda_index(t, name):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
-def _same_device(ref, **tensors):
+def _on(index, **tensors):
+    """Every tensor given lies on CUDA device `index`."""
     for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != ref.device):
-            raise ValueError(f"{name} must be a CUDA tensor on {ref.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
 
 
-def _lens(B, **tensors):
+def _lens(B, index, **tensors):
     for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1
-                              or t.shape[0] != B or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B entries")
+        if t is not None and (t.dtype != torch.int32 or t.get_device() != index
+                              or t.shape != (B,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of B entries on "
+                             f"cuda:{index}")
 
 
 def _weights_tensor(t, shape, name):
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape
                           or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
 
@@ -501,22 +512,27 @@ def mea_kv4_alloc(B: int, cache_rows: int, Hkv: int, K: int, dtype=torch.bfloat1
 
 
 def _kv4_dims(cache: Kv4Cache, what="cache"):
-    """(B, Hkv, rows, K, dtype) of a 4-bit cache, checked."""
+    """(B, Hkv, rows, K, dtype, device index) of a 4-bit cache, checked."""
     kc, kp, vc, vp = cache
-    if kc.dim() != 4 or kc.dtype != torch.uint8:
+    shape = kc.shape
+    if len(shape) != 4 or kc.dtype != torch.uint8:
         raise ValueError(f"{what}: codes must be uint8 [B, Hkv, rows, K/2]")
-    B, Hkv, rows, half = kc.shape
-    K = 2 * half
-    if kp.dtype not in _DTYPE or vp.dtype != kp.dtype:
+    B, Hkv, rows, half = shape
+    dtype = kp.dtype
+    if dtype not in _DTYPE or vp.dtype != dtype:
         raise ValueError(f"{what}: params must share dtype float16 or bfloat16")
-    if vc.dtype != torch.uint8 or tuple(vc.shape) != tuple(kc.shape):
+    if vc.dtype != torch.uint8 or vc.shape != shape:
         raise ValueError(f"{what}: k_codes and v_codes must be alike")
-    if K % 64 or any(tuple(t.shape) != (B, Hkv, rows, K // 64, 2) for t in (kp, vp)):
+    want = (B, Hkv, rows, half // 32, 2)
+    if half % 32 or kp.shape != want or vp.shape != want:
         raise ValueError(f"{what}: params must be [B, Hkv, rows, K/64, 2]")
-    if not all(t.is_contiguous() for t in cache):
+    if not (kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous()
+            and vp.is_contiguous()):
         raise ValueError(f"{what}: the planes must be contiguous")
-    _same_device(kc, k_params=kp, v_codes=vc, v_params=vp)
-    return B, Hkv, rows, K, kp.dtype
+    index = _cuda_index(kc, what)
+    if kp.get_device() != index or vc.get_device() != index or vp.get_device() != index:
+        raise ValueError(f"{what}: the planes must lie on one device")
+    return B, Hkv, rows, 2 * half, dtype, index
 
 
 def mea_kv4_append(k_new, v_new, cache: Kv4Cache, cache_seqlens, q_seqlens=None, stream=None):
@@ -524,19 +540,20 @@ def mea_kv4_append(k_new, v_new, cache: Kv4Cache, cache_seqlens, q_seqlens=None,
     cache_seqlens / q_seqlens int32 CUDA [B] (rows already there, and rows of the chunk, M
     if None): rows cache_seqlens[b] .. + q_seqlens[b] of the cache are written.  The caller
     advances cache_seqlens.  Returns the cache."""
-    B, Hkv, rows, K, dtype = _kv4_dims(cache)
-    M = k_new.shape[1] if k_new.dim() == 4 else 0
-    if tuple(k_new.shape) != (B, M, Hkv, K) or tuple(v_new.shape) != (B, M, Hkv, K):
+    B, Hkv, rows, K, dtype, index = _kv4_dims(cache)
+    shape = k_new.shape
+    M = shape[1] if len(shape) == 4 else 0
+    if shape != (B, M, Hkv, K) or v_new.shape != shape:
         raise ValueError("k_new and v_new must be [B, M, Hkv, K]")
     if k_new.dtype != dtype or v_new.dtype != dtype:
         raise ValueError("k_new and v_new must have the dtype of the cache's params")
-    _same_device(cache.k_codes, k_new=k_new, v_new=v_new, cache_seqlens=cache_seqlens,
-                 q_seqlens=q_seqlens)
-    _lens(B, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
-    _launch("mea_kv4_append", lib.mea_kv4_append, k_new.device, stream, (),
-            (_ptr(k_new), _ptr(v_new), *map(_ptr, cache), _ptr(cache_seqlens), _ptr(q_seqlens),
-             B, M, rows, Hkv, K, _bmhk_strides(k_new, "k_new"), _bmhk_strides(v_new, "v_new"),
-             _DTYPE[dtype]))
+    _on(index, k_new=k_new, v_new=v_new)
+    _lens(B, index, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    kc, kp, vc, vp = cache
+    _launch("mea_kv4_append", lib.mea_kv4_append, index, stream, (),
+            (k_new.data_ptr(), v_new.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(),
+             vp.data_ptr(), cache_seqlens.data_ptr(), _addr(q_seqlens), B, M, rows, Hkv, K,
+             _bmhk_strides(k_new, "k_new"), _bmhk_strides(v_new, "v_new"), _DTYPE[dtype]))
     return cache
 
 
@@ -545,7 +562,7 @@ def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
     """Rows first_rows[b] .. + rows[b] (from row 0 if None) of a 4-bit cache in 16 bits:
     (k, v), each [B, out_rows, Hkv, K] (out_rows defaults to the cache's rows, or to that of
     k_out); rows past rows[b] are not written."""
-    B, Hkv, cap, K, dtype = _kv4_dims(cache)
+    B, Hkv, cap, K, dtype, index = _kv4_dims(cache)
     if out_rows is None:
         ref = k_out if k_out is not None else v_out
         out_rows = cap if ref is None else ref.shape[1]
@@ -557,15 +574,16 @@ def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
         fresh.append(v_out)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if tuple(t.shape) != shape or t.dtype != dtype:
-            raise ValueError(f"{name} must be {list(shape)} of the params' dtype")
-    _same_device(cache.k_codes, k_out=k_out, v_out=v_out, rows=rows, first_rows=first_rows)
-    _lens(B, rows=rows, first_rows=first_rows)
-    _launch("mea_kv4_read", lib.mea_kv4_read, k_out.device, stream, fresh,
-            (*map(_ptr, cache), _ptr(rows), _ptr(first_rows), _ptr(k_out), _ptr(v_out), B, cap,
-             shape[1], Hkv, K, _bmhk_strides(k_out, "k_out"), _bmhk_strides(v_out, "v_out"),
-             _DTYPE[dtype]))
+    if k_out.shape != shape or v_out.shape != shape or k_out.dtype != dtype \
+            or v_out.dtype != dtype:
+        raise ValueError(f"k_out and v_out must be {list(shape)} of the params' dtype")
+    _on(index, k_out=k_out, v_out=v_out)
+    _lens(B, index, rows=rows, first_rows=first_rows)
+    kc, kp, vc, vp = cache
+    _launch("mea_kv4_read", lib.mea_kv4_read, index, stream, fresh,
+            (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), rows.data_ptr(),
+             _addr(first_rows), k_out.data_ptr(), v_out.data_ptr(), B, cap, shape[1], Hkv, K,
+             _bmhk_strides(k_out, "k_out"), _bmhk_strides(v_out, "v_out"), _DTYPE[dtype]))
     return k_out, v_out
 
 
@@ -586,46 +604,56 @@ def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float
     fp32 = ``weights`` (zeros if None) + the softmax weight each row got in this step, summed
     over the query heads of its kv head; 0 for rows past kv_seqlens[b].  weights_out may be
     weights itself."""
-    B, Hkv, cap, K, dtype = _kv4_dims(cache)
-    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1) or q.shape[0] != B \
-            or q.shape[-1] != K:
+    B, Hkv, cap, K, dtype, index = _kv4_dims(cache)
+    shape = q.shape
+    if len(shape) not in (3, 4) or (len(shape) == 4 and shape[1] != 1) or shape[0] != B \
+            or shape[-1] != K:
         raise ValueError("q must be [B, Hq, K] or [B, 1, Hq, K]")
-    Hq = q.shape[-2]
+    Hq = shape[-2]
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if q.dtype != dtype:
         raise ValueError("q must have the dtype of the cache's params")
     scale = K ** -0.5 if scale is None else float(scale)
-    dev, fresh = q.device, []
+    max_kv_len, fresh = int(max_kv_len), []
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=dtype, device=dev)
+        out = torch.empty_like(q)
         fresh.append(out)
-    if tuple(out.shape) != tuple(q.shape) or out.dtype != dtype or not out.is_contiguous():
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped and typed like q")
-    if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _weights_tensor(lse, (B, Hq), "lse")
+    elif return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
         fresh.append(lse)
-    _weights_tensor(lse, (B, Hq), "lse")
     want = return_weights or weights_out is not None
     if weights is not None and not want:
         raise ValueError("weights needs return_weights or weights_out")
-    if want and weights_out is None:
-        weights_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=dev)
-        fresh.append(weights_out)
-    _weights_tensor(weights, (B, Hkv, cap), "weights")
-    _weights_tensor(weights_out, (B, Hkv, cap), "weights_out")
-    _same_device(q, cache=cache.k_codes, kv_seqlens=kv_seqlens, out=out, lse=lse, weights=weights,
-                 weights_out=weights_out, workspace=workspace)
-    _lens(B, kv_seqlens=kv_seqlens)
-    need = mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, want)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        fresh.append(workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch("mea_decode_kv4", lib.mea_decode_kv4, dev, stream, fresh,
-            (_ptr(q), *map(_ptr, cache), _ptr(kv_seqlens), _ptr(out), _ptr(lse), _ptr(weights),
-             _ptr(weights_out), B, Hq, Hkv, K, cap, int(max_kv_len), _DTYPE[dtype],
-             int(bool(alibi)), scale, _ptr(workspace), ws_bytes))
+    if want:
+        if weights_out is None:
+            weights_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=q.device)
+            fresh.append(weights_out)
+        _weights_tensor(weights, (B, Hkv, cap), "weights")
+        _weights_tensor(weights_out, (B, Hkv, cap), "weights_out")
+    _on(index, q=q, out=out, lse=lse, weights=weights, weights_out=weights_out,
+        workspace=workspace)
+    _lens(B, index, kv_seqlens=kv_seqlens)
+    ws_bytes = 0
+    if workspace is None:
+        need = mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, want)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            fresh.append(workspace)
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    kc, kp, vc, vp = cache
+    _launch("mea_decode_kv4", lib.mea_decode_kv4, index, stream, fresh,
+            (q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
+             kv_seqlens.data_ptr(), out.data_ptr(), _addr(lse), _addr(weights),
+             _addr(weights_out), B, Hq, Hkv, K, cap, max_kv_len, _DTYPE[dtype],
+             1 if alibi else 0, scale, _addr(workspace), ws_bytes))
     return (out, lse, weights_out) if want else (out, lse)
 
 
@@ -641,13 +669,15 @@ def mea_key_weights(q, k, lse, cache_seqlens=None, q_seqlens=None, causal: bool 
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, M, Hq, K] and k [B, N, Hkv, K]")
     B, M, Hq, K = q.shape
-    N, Hkv = k.shape[1], k.shape[2]
-    if tuple(k.shape) != (B, N, Hkv, K):
+    _, N, Hkv, _ = k.shape
+    if k.shape != (B, N, Hkv, K):
         raise ValueError("k must be [B, N, Hkv, K]")
     if q.dtype not in _DTYPE or k.dtype != q.dtype:
         raise ValueError("q and k must share dtype float16 or bfloat16")
     if q_seqlens is not None and cache_seqlens is None:
         raise ValueError("q_seqlens needs cache_seqlens")
+    if lse is None:
+        raise ValueError("lse must be what the attention of these queries returned")
     _weights_tensor(lse, (B, Hq, M), "lse")
     scale = K ** -0.5 if scale is None else float(scale)
     fresh = []
@@ -656,22 +686,23 @@ def mea_key_weights(q, k, lse, cache_seqlens=None, q_seqlens=None, causal: bool 
         fresh.append(out)
     _weights_tensor(weights, (B, Hkv, N), "weights")
     _weights_tensor(out, (B, Hkv, N), "out")
-    _same_device(q, k=k, lse=lse, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens,
-                 weights=weights, out=out)
-    _lens(B, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
-    _launch("mea_key_weights", lib.mea_key_weights, q.device, stream, fresh,
-            (_ptr(q), _ptr(k), _ptr(lse), _ptr(cache_seqlens), _ptr(q_seqlens), _ptr(weights),
-             _ptr(out), B, M, N, Hq, Hkv, K, _bmhk_strides(q, "q"), _bmhk_strides(k, "k"),
-             _DTYPE[q.dtype], int(bool(causal)), int(bool(alibi)), scale))
+    index = _cuda_index(q, "q")
+    _on(index, k=k, lse=lse, weights=weights, out=out)
+    _lens(B, index, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    _launch("mea_key_weights", lib.mea_key_weights, index, stream, fresh,
+            (q.data_ptr(), k.data_ptr(), lse.data_ptr(), _addr(cache_seqlens), _addr(q_seqlens),
+             _addr(weights), out.data_ptr(), B, M, N, Hq, Hkv, K, _bmhk_strides(q, "q"),
+             _bmhk_strides(k, "k"), _DTYPE[q.dtype], 1 if causal else 0, 1 if alibi else 0,
+             scale))
     return out
 
 
 def _planes_of(cache, what):
-    """A cache as ([(tensor, (row axis, head axis))], B, Hkv, rows): a Kv4Cache, or a
+    """A cache as ([(tensor, (row axis, head axis))], B, Hkv, rows, device): a Kv4Cache, or a
     (k_cache, v_cache) pair of [B, rows, Hkv, K] tensors with contiguous K."""
     if isinstance(cache, Kv4Cache):
-        B, Hkv, rows, _, _ = _kv4_dims(cache, what)
-        return [(t, (2, 1)) for t in cache], B, Hkv, rows
+        B, Hkv, rows, _, _, index = _kv4_dims(cache, what)
+        return [(t, (2, 1)) for t in cache], B, Hkv, rows, index
     k, v = cache
     for name, t in (("k", k), ("v", v)):
         if t.dim() != 4 or t.stride(3) != 1:
@@ -680,8 +711,9 @@ def _planes_of(cache, what):
             raise ValueError(f"{what}: {name} must be float16 or bfloat16")
     if k.shape[:3] != v.shape[:3]:
         raise ValueError(f"{what}: k and v must have the same rows and heads")
-    _same_device(k, v=v)
-    return [(k, (1, 2)), (v, (1, 2))], k.shape[0], k.shape[2], k.shape[1]
+    index = _cuda_index(k, what)
+    _on(index, v=v)
+    return [(k, (1, 2)), (v, (1, 2))], k.shape[0], k.shape[2], k.shape[1], index
 
 
 def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out=None,
@@ -695,16 +727,18 @@ def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out
     weights are cut in place too).  Returns (new_seqlens int32 [B], kept int32 [B,Hkv,budget]
     -- the old row of every kept row, -1 after the last --, weights_out [B,Hkv,out rows], 0
     past the kept rows)."""
-    src, B, Hkv, rows = _planes_of(cache, "cache")
+    src, B, Hkv, rows, index = _planes_of(cache, "cache")
     if out is None:
         dst, out_rows = src, rows
         if weights_out is not None and weights_out.data_ptr() != weights.data_ptr():
             raise ValueError("in place, weights are cut in place too")
         weights_out = weights
     else:
-        dst, Bo, Ho, out_rows = _planes_of(out, "out")
+        dst, Bo, Ho, out_rows, out_index = _planes_of(out, "out")
         if isinstance(cache, Kv4Cache) != isinstance(out, Kv4Cache) or (Bo, Ho) != (B, Hkv):
             raise ValueError("out must be a cache of the same kind, batch and heads")
+        if out_index != index:
+            raise ValueError(f"out must lie on cuda:{index}")
     budget, recent = int(budget), int(recent)
     dev, fresh = src[0][0].device, []
     if weights_out is None:
@@ -718,24 +752,23 @@ def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out
         fresh.append(kept)
     _weights_tensor(weights, (B, Hkv, rows), "weights")
     _weights_tensor(weights_out, (B, Hkv, out_rows), "weights_out")
-    if kept.dtype != torch.int32 or tuple(kept.shape) != (B, Hkv, budget) \
-            or not kept.is_contiguous():
+    if kept.dtype != torch.int32 or kept.shape != (B, Hkv, budget) or not kept.is_contiguous():
         raise ValueError("kept must be a contiguous int32 [B, Hkv, budget] tensor")
-    _same_device(src[0][0], weights=weights, weights_out=weights_out, kept=kept,
-                 cache_seqlens=cache_seqlens, new_seqlens=new_seqlens, out=dst[0][0])
-    _lens(B, cache_seqlens=cache_seqlens, new_seqlens=new_seqlens)
+    _on(index, weights=weights, weights_out=weights_out, kept=kept)
+    _lens(B, index, cache_seqlens=cache_seqlens, new_seqlens=new_seqlens)
     planes = (_Plane * len(src))()
     for p, ((s, (r, h)), (d, _)) in enumerate(zip(src, dst)):
         if s.dtype != d.dtype or s.shape[3:] != d.shape[3:]:
             raise ValueError("out must have the rows of the cache")
-        size = s.element_size()
+        size, ss, ds = s.element_size(), s.stride(), d.stride()
         planes[p] = _Plane(s.data_ptr(), d.data_ptr(),
-                           _i64x3(*(s.stride(x) * size for x in (0, r, h))),
-                           _i64x3(*(d.stride(x) * size for x in (0, r, h))),
-                           s[0, 0, 0].numel() * size if s.numel() else 0)
-    _launch("mea_cache_evict", lib.mea_cache_evict, dev, stream, fresh,
-            (planes, len(src), _ptr(weights), _ptr(weights_out), _ptr(cache_seqlens),
-             _ptr(new_seqlens), _ptr(kept), B, Hkv, rows, out_rows, budget, recent))
+                           _i64x3(ss[0] * size, ss[r] * size, ss[h] * size),
+                           _i64x3(ds[0] * size, ds[r] * size, ds[h] * size),
+                           s.shape[3:].numel() * size)
+    _launch("mea_cache_evict", lib.mea_cache_evict, index, stream, fresh,
+            (planes, len(src), weights.data_ptr(), weights_out.data_ptr(),
+             cache_seqlens.data_ptr(), new_seqlens.data_ptr(), kept.data_ptr(), B, Hkv, rows,
+             out_rows, budget, recent))
     return new_seqlens, kept, weights_out
 
 
