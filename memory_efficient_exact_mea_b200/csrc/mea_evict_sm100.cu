@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelTile = 4 * kSelThreads;
+constexpr int kSelHeld = 8;  // keys a thread holds: up to 8192 rows are read once
 constexpr int kBins = 2048;
 
 // An unsigned integer ordered as the float is; NaN below everything, -0 as 0.
@@ -60,6 +61,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   for (int r = tid; r < a.recent; r += kSelThreads) kept[take + r] = m + r;
   if (take == 0) return;
 
+  const bool held = m <= kSelHeld * kSelThreads;
+  uint32_t mine[kSelHeld];
+  if (held) {
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u) {
+      const int j = u * kSelThreads + tid;
+      mine[u] = j < m ? order_key(w[j]) : 0u;
+    }
+  }
   uint32_t prefix = 0, need = take;  // rows still to find among those with this prefix
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
@@ -68,10 +78,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int above = pass == 0 ? 0 : pass == 1 ? 21 : 10;  // bits already fixed start here
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-#pragma unroll 8
-    for (int j = tid; j < m; j += kSelThreads) {
-      const uint32_t key = order_key(w[j]);
+    auto count = [&](uint32_t key) {
       if (pass == 0 || (key >> above) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1u);
+    };
+    if (held) {
+#pragma unroll
+      for (int u = 0; u < kSelHeld; ++u)
+        if (u * kSelThreads + tid < m) count(mine[u]);
+    } else {
+      for (int j0 = tid; j0 < m; j0 += kSelHeld * kSelThreads) {
+        float x[kSelHeld];  // all in flight before the first is counted
+#pragma unroll
+        for (int u = 0; u < kSelHeld; ++u)
+          x[u] = j0 + u * kSelThreads < m ? w[j0 + u * kSelThreads] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kSelHeld; ++u)
+          if (j0 + u * kSelThreads < m) count(order_key(x[u]));
+      }
     }
     __syncthreads();
     // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t

@@ -30,6 +30,18 @@ __device__ __forceinline__ float to_f(uint32_t x) {  // low 16 bits
 }
 
 template <bool BF16>
+__device__ __forceinline__ float step_of(uint32_t w) {  // low 16 bits of a pair
+  if constexpr (BF16) return __uint_as_float(w << 16);
+  else return __low2float(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float zero_of(uint32_t w) {  // high 16 bits of a pair
+  if constexpr (BF16) return __uint_as_float(w & 0xffff0000u);
+  else return __high2float(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <bool BF16>
 __device__ __forceinline__ uint32_t to_16(float x) {
   if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
   else return __half_as_ushort(__float2half_rn(x));
@@ -79,27 +91,28 @@ __device__ __noinline__ float code_wide(float x, float z, float s) {
   return static_cast<float>(rint((static_cast<double>(x) - z) / s));
 }
 
+// Packed minimum and maximum; a NaN stays one.
 template <bool BF16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   if constexpr (BF16) {
-    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
     const __half2 r =
-        __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   if constexpr (BF16) {
-    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
     const __half2 r =
-        __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
 }
@@ -132,6 +145,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   uint32_t* codes = static_cast<uint32_t*>(value ? a.v_codes : a.k_codes) + dst * kLanes + part;
   uint32_t* params =
       static_cast<uint32_t*>(value ? a.v_params : a.k_params) + dst * (D / 64) + part / 8;
+  static_assert(kRowGroup <= 8, "a lane of the eight for each row");
 
   uint4 raw[kRowGroup];
 #pragma unroll
@@ -139,38 +153,54 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     raw[u] = make_uint4(0, 0, 0, 0);
     if (u < rows) raw[u] = *reinterpret_cast<const uint4*>(src + u * step);
   }
+  // Least and greatest value of each row's group, in all its eight lanes; lane u of
+  // the eight then keeps those of row u and works out its step alone.
+  float z_row[kRowGroup], top = 0.f, low = 0.f;
+  const int lane8 = threadIdx.x & 7;
 #pragma unroll
   for (int u = 0; u < kRowGroup; ++u) {
-    if (__all_sync(0xffffffffu, u >= rows)) break;  // no row left for any lane
-    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-    float x[8], bad = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = BF16 ? __uint_as_float(w[i] << 16) : to_f<BF16>(w[i] & 0xffffu);
-      x[2 * i + 1] = BF16 ? __uint_as_float(w[i] & 0xffff0000u) : to_f<BF16>(w[i] >> 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bad = fmaf(x[i], 0.f, bad);  // NaN once a value is not finite
-    uint32_t lo = min2<BF16>(min2<BF16>(w[0], w[1]), min2<BF16>(w[2], w[3]));
-    uint32_t hi = max2<BF16>(max2<BF16>(w[0], w[1]), max2<BF16>(w[2], w[3]));
+    uint32_t lo = min2<BF16>(min2<BF16>(raw[u].x, raw[u].y), min2<BF16>(raw[u].z, raw[u].w));
+    uint32_t hi = max2<BF16>(max2<BF16>(raw[u].x, raw[u].y), max2<BF16>(raw[u].z, raw[u].w));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       lo = min2<BF16>(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max2<BF16>(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    const float mn = fminf(to_f<BF16>(lo & 0xffffu), to_f<BF16>(lo >> 16));
-    const float mx = fmaxf(to_f<BF16>(hi & 0xffffu), to_f<BF16>(hi >> 16));
-    const unsigned bad_lanes = __ballot_sync(0xffffffffu, bad != bad);
-    const bool bad_group = ((bad_lanes >> (threadIdx.x & 24)) & 0xffu) != 0;
-    const float range = mx - mn;  // may pass fp32's largest value for bf16 inputs
-    const float s_raw = isinf(range) ? (0.5f * mx - 0.5f * mn) / 15.f * 2.f : range / 15.f;
-    uint32_t s16 = to_16<BF16>(s_raw), z16 = to_16<BF16>(mn);
-    const float s = to_f<BF16>(s16), z = mn;
+    lo = min2<BF16>(lo, lo >> 16);  // (the high half is not used)
+    hi = max2<BF16>(hi, hi >> 16);
+    z_row[u] = to_f<BF16>(lo & 0xffffu);
+    if (lane8 == u) {
+      low = z_row[u];
+      top = to_f<BF16>(hi & 0xffffu);
+    }
+  }
+  const float range = top - low;  // may pass fp32's largest value for bf16 inputs
+  const float s_raw = isinf(range) ? (0.5f * top - 0.5f * low) / 15.f * 2.f : range / 15.f;
+  uint32_t s16 = to_16<BF16>(s_raw), z16 = to_16<BF16>(low);
+  const float s_mine = to_f<BF16>(s16);
+  // 1/s within 2 ulp, like the 1e-4 next to a half below; 0: codes of zero; negative:
+  // steps whose reciprocal or whose x - z could leave fp32's range
+  float inv_mine = 0.f;
+  if (!(fabsf(low) < __int_as_float(0x7f800000) && fabsf(top) < __int_as_float(0x7f800000)))
+    s16 = z16 = BF16 ? 0x7fc0u : 0x7e00u;  // a group with a NaN or infinity stands for NaN
+  else if (s_mine > 0.f)
+    inv_mine = s_mine >= 0x1p-100f && s_mine <= 0x1p100f ? __fdividef(1.f, s_mine) : -1.f;
+  if (lane8 < rows) params[lane8 * (D / 64)] = s16 | (z16 << 16);
+
+#pragma unroll
+  for (int u = 0; u < kRowGroup; ++u) {
+    const float inv = __shfl_sync(0xffffffffu, inv_mine, u, 8);
+    const float s = __shfl_sync(0xffffffffu, s_mine, u, 8), z = z_row[u];
+    if (u >= rows) continue;
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = step_of<BF16>(w[i]);
+      x[2 * i + 1] = zero_of<BF16>(w[i]);
+    }
     uint32_t word = 0;
-    if (bad_group) {
-      s16 = z16 = BF16 ? 0x7fc0u : 0x7e00u;  // a group with a NaN or infinity stands for NaN
-    } else if (s >= 0x1p-100f && s <= 0x1p100f) {
-      const float inv = __fdividef(1.f, s);  // within 2 ulp, like the 1e-4 next to a half
+    if (inv > 0.f) {
       float worst = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -183,20 +213,23 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
       constexpr uint32_t kBits = 0x4B400000u;
       word -= kBits + (kBits << 4) + (kBits << 8) + (kBits << 12) + (kBits << 16) +
               (kBits << 20) + (kBits << 24) + (kBits << 28);
-      if (worst > 0.4999f) {  // a quotient next to a half (or past 15)
-        word = 0;
+      if (worst > 0.4999f) {  // some quotient lies next to a half, or past 15
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          word |= static_cast<uint32_t>(fminf(code_near_half(x[i], z, s, inv), 15.f)) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+          const float d = x[i] - z;
+          const float m = fminf(fmaf(d, inv, kRound), kRound + 15.f);
+          if (fabsf(fmaf(d, inv, kRound - m)) > 0.4999f) {
+            const uint32_t c =
+                static_cast<uint32_t>(fminf(code_near_half(x[i], z, s, inv), 15.f));
+            word = (word & ~(15u << (4 * i))) | (c << (4 * i));
+          }
+        }
       }
-    } else if (s > 0.f) {
+    } else if (inv < 0.f) {
       for (int i = 0; i < 8; ++i)
         word |= static_cast<uint32_t>(fminf(fmaxf(code_wide(x[i], z, s), 0.f), 15.f)) << (4 * i);
     }
-    if (u < rows) {
-      codes[u * kLanes] = word;
-      if (part % 8 == 0) params[u * (D / 64)] = s16 | (z16 << 16);
-    }
+    codes[u * kLanes] = word;
   }
 }
 
@@ -296,17 +329,20 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 //
 // Both products run in fp16 whatever the input type.  q is scaled by a power of two to
 // a largest magnitude below 256, exact but for values 2^-22 of that and less.
-// P' = p s is rounded to fp16 (11 bits, finer than a bf16 result's 8; mea_decode
-// rounds p the same way for fp16): the reference R of p = 2^(y - R) is chosen per
-// head so that the largest p s is about one, not the largest p, and is raised only
-// when some p s passes 2^14 (so the accumulators are rarely rescaled).
+// P' = p s goes in as one fp16 number for bf16 results (11 bits against the result's
+// 8: the error against 64 bits stays at the result's own rounding) and as two, high
+// and low, for fp16 results (one would double their error).  The reference R of
+// p = 2^(y - R) is chosen per head so that the largest p s is about one, not the
+// largest p, and is raised only when some p s passes 2^14 (so the accumulators are
+// rarely rescaled).
 //
-// A warp takes 32 rows at a time in the fragment layout of mma.sync m16n8k16 (rows x heads and dimensions x heads, heads padded to
-// 8): a thread's nibbles for one row are whole words of the row, and since the order
-// of the contraction index is free, the pairs (i, i + 4) of a word serve as the
-// operand's pairs.  V pairs two rows: one byte permute joins the halves of the two
-// rows' words.  Each warp copies its own tiles into a ring of its own (cp.async,
-// 16-byte chunks, no barrier but __syncwarp), two tiles ahead.
+// A warp takes 32 rows at a time in the fragment layout of mma.sync m16n8k16 (rows
+// x heads and dimensions x heads, heads padded to 8): a thread's nibbles for one
+// row are whole words of the row, and since the order of the contraction index is
+// free, the pairs (i, i + 4) of a word serve as the operand's pairs.  V pairs two
+// rows: one byte permute joins the halves of the two rows' words.  Each warp copies
+// its own tiles into a ring of its own (cp.async, 16-byte chunks, no barrier but
+// __syncwarp), two tiles ahead.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -381,18 +417,6 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t* r) {
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ float step_of(uint32_t w) {  // low 16 bits
-  if constexpr (BF16) return __uint_as_float(w << 16);
-  else return __low2float(*reinterpret_cast<const __half2*>(&w));
-}
-
-template <bool BF16>
-__device__ __forceinline__ float zero_of(uint32_t w) {  // high 16 bits
-  if constexpr (BF16) return __uint_as_float(w & 0xffff0000u);
-  else return __high2float(*reinterpret_cast<const __half2*>(&w));
-}
-
 constexpr int kStages = 3;  // ring of one warp: one tile in use, two in flight
 
 template <int D>
@@ -419,7 +443,7 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 }
 
 template <int D, bool BF16, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = KSmem<D>;
   constexpr int NG = L::NG;  // groups of a row
   extern __shared__ __align__(128) uint8_t smem[];
@@ -676,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
     }
     // Weights of the tile against the present reference: p s in fp16, and the sums
     // of p, p s and p z (an overflow shows in a sum of numbers >= 0).
-    uint32_t pk[2][NG][2];
+    constexpr int kParts = BF16 ? 1 : 2;
+    uint32_t pk[2][NG][2][kParts];
     float sum[2], heavy[2], zsum[NG][2];
     auto weigh = [&] {
 #pragma unroll
@@ -692,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
         for (int e = 0; e < 2; ++e)
           p[e] = ex2(fmaf(y[i >> 1][2 * (i & 1) + e], unit[e], -ref[e]));
         if (last) {
-          asm volatile("" ::: "memory");  // a branch, not selects in every tile
+          asm volatile("");  // a branch, not selects in every tile
           if (t + 8 * i + gid >= s1) p[0] = p[1] = 0.f;
         }
 #pragma unroll
@@ -703,7 +728,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
           heavy[1] += ps1;
           zsum[g][0] = fmaf(p[0], z, zsum[g][0]);
           zsum[g][1] = fmaf(p[1], z, zsum[g][1]);
-          pk[i >> 1][g][i & 1] = pack2<false>(ps0, ps1);
+          uint32_t(&out)[kParts] = pk[i >> 1][g][i & 1];
+          out[0] = pack2<false>(ps0, ps1);
+          if constexpr (kParts == 2)
+            out[1] = pack2<false>(ps0 - step_of<false>(out[0]), ps1 - zero_of<false>(out[0]));
         }
         sum[0] += p[0];
         sum[1] += p[1];
@@ -712,9 +740,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
     weigh();
     if (__any_sync(0xffffffffu, heavy[0] > kMaxWeight || heavy[1] > kMaxWeight ||
                                     sum[0] > kMaxPlain || sum[1] > kMaxPlain)) {
-      // Raise the reference: the largest p s of these rows becomes about one.  A
-      // row whose step is small beside its zero counts with 2^-12 of the zero, so
-      // that p z stays in range too.
+      // Raise the reference: the largest p s of these rows becomes about one, and p
+      // of that row a power of two (a lone row's lse is then exact).  A row whose
+      // step is small beside its zero counts with 2^-12 of the zero, so that p z
+      // stays in range too.
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float v = neg_inf();
@@ -725,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
           for (int g = 0; g < NG; ++g)
             mag = fmaxf(mag, fmaxf(step_of<BF16>(vq[i][g]),
                                    fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f));
-          v = fmaxf(v, fmaf(y[i >> 1][2 * (i & 1) + e], unit[e], __log2f(mag)));
+          v = fmaxf(v, y[i >> 1][2 * (i & 1) + e] * unit[e] + rintf(__log2f(mag)));
         }
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
@@ -754,9 +783,12 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
       zacc[g][1] += zsum[g][1];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
-        uint32_t pb[2];
-        pb[0] = movmatrix_trans(pk[blk][g][0]);
-        pb[1] = movmatrix_trans(pk[blk][g][1]);
+        uint32_t pb[kParts][2];
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          pb[part][0] = movmatrix_trans(pk[blk][g][0][part]);
+          pb[part][1] = movmatrix_trans(pk[blk][g][1][part]);
+        }
         // rows 2 tig, 2 tig + 1 (first pair) and + 8 (second): words of 8 dimensions
         uint32_t w0, w1, w2, w3;
         lds<4>(st + v_at[0][g] + blk * 8 * D, &w0);
@@ -769,7 +801,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
         const CodePairs yb = code_pairs(__byte_perm(w2, w3, 0x7632));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[0], pb[1]);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+            mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[part][0],
+                        pb[part][1]);
       }
     }
   }
@@ -817,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const Kv4Decode
     }
     const long long row = static_cast<long long>(b) * a.Hq + h0 + g;
     const float val = lsum == 0.f ? 0.f : o / lsum;  // a NaN stays a NaN
-    const float lse2 = lsum == 0.f ? neg_inf() : mx + __log2f(lsum);
+    const float lse2 = lsum == 0.f ? neg_inf() : mx + log2f(lsum);
     if (a.part_o == nullptr) {  // the only split
       static_cast<uint16_t*>(a.out)[row * D + d] = static_cast<uint16_t>(to_16<BF16>(val));
     } else {
@@ -846,7 +881,7 @@ __device__ __forceinline__ float merged_lse2(const float* pl, int ns, int lane) 
   for (int s = lane; s < ns; s += 32) sum += ex2(pl[s] - base);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum == 0.f ? neg_inf() : base + __log2f(sum);
+  return sum == 0.f ? neg_inf() : base + log2f(sum);
 }
 
 template <int D, bool BF16>

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
       [[maybe_unused]] const float slope = ALIBI ? s_slope[ls] : 0.f;
       // `open`: every column of the tile counts for every key of it
       auto add_tile = [&](auto open) {
-#pragma unroll 1
+#pragma unroll 2
         for (int c0 = 0; c0 < NQ; c0 += 32) {
           uint32_t r[32];
           tmem_ld32(tmem_base + buf * NQ + c0 + lane_addr, r);
