@@ -366,21 +366,6 @@ __device__ __forceinline__ void mma_f16_acc(float (&d)[4], uint32_t a0, uint32_t
   mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
-// One product of the input type, A rows (gid, gid + 8) with k = 2 tig, 2 tig + 1 only.
-template <bool BF16>
-__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5}, {%6}, {%7, %7, %7, %7};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
-  else
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5}, {%6}, {%7, %7, %7, %7};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
-}
-
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -527,10 +512,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
   }
 
   // Q^T as the B operand (head gid), scaled; the sums of q that go with the zeros,
-  // in three pieces of the input type (exact to fp32) as the operand of one more
-  // product.
-  uint32_t qb[NG][4][2], qz = 0u;
-  float scl[2];
+  // for this thread's two heads (2 tig, 2 tig + 1).
+  uint32_t qb[NG][4][2];
+  float qsum[NG][2], scl[2];
   {
     const uint4* qrow = reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(a.q) +
@@ -552,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 1));
     big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
     const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
-    // 2^k with the largest |q| 2^k in [128, 256), 1 where q is zero or not finite; fp16
-    // numbers are only made smaller (their sums, in fp16 pieces, must fit)
+    // 2^k with the largest |q| 2^k in [128, 256), 1 where q is zero or not finite (16
+    // times that must fit fp16)
     int k = 0;
     if (BF16 && big != 0u && big < 0x7f80u) k = 134 - static_cast<int>(big >> 7);
-    if (!BF16 && big < 0x7c00u) k = min(22 - static_cast<int>(big >> 10), 0);
+    if (!BF16 && big != 0u && big < 0x7c00u) k = min(22 - static_cast<int>(big >> 10), 15);
     k = min(max(k, -126), 126);
     const float f = __int_as_float((127 + k) << 23), inv = __int_as_float((127 - k) << 23);
 #pragma unroll
@@ -577,13 +561,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
         }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      // piece tig of the sum, for k = 2 tig + g (one group: k = 2 tig + 1)
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const uint32_t piece = to_16<BF16>(sum);
-        sum -= to_f<BF16>(piece);
-        if (tig == i) qz |= piece << (NG == 2 ? 16 * g : 16);
-      }
+      for (int e = 0; e < 2; ++e) qsum[g][e] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * e);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -643,19 +622,17 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     }
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-      // the zeros' share: A holds (z of group 0, z of group 1), or (s, z) against (0, q)
-      const uint32_t(&lo)[NG] = kq[2 * blk];
-      const uint32_t(&hi)[NG] = kq[2 * blk + 1];
-      mma_zero<BF16>(y[blk], NG == 2 ? __byte_perm(lo[0], lo[NG - 1], 0x7632) : lo[0],
-                     NG == 2 ? __byte_perm(hi[0], hi[NG - 1], 0x7632) : hi[0], qz);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const float s = step_of<BF16>(kq[2 * blk + r][g]) * kUnitOdd;
+          const float z = zero_of<BF16>(kq[2 * blk + r][g]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            y[blk][2 * r + e] = fmaf(s, sc[blk][g][2 * r + e], y[blk][2 * r + e]);
+          for (int e = 0; e < 2; ++e) {
+            float& yy = y[blk][2 * r + e];
+            yy = fmaf(s, sc[blk][g][2 * r + e], g == 0 ? z * qsum[g][e] : fmaf(z, qsum[g][e], yy));
+          }
         }
     }
   };
