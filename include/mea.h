@@ -343,7 +343,9 @@ int mea_bwd_stages(const void* q, const void* k, const void* v, const void* out,
  *   k_new, v_new  [B, M, Hkv, K] element strides (b, m, h), K contiguous; rows >= n unused
  *   cache_seqlens DEVICE int32 [B], not updated (the caller adds n afterwards)
  * A sequence with past < 0, n outside [0, M] or past + n > cache_rows is skipped
- * and records MEA_ERR_INVALID_ARG in the device status word.
+ * and records MEA_ERR_INVALID_ARG in the device status word.  Here and below, a
+ * sequence of more than 2^30 rows or a batch of 2^31 rows x heads returns
+ * MEA_ERR_UNSUPPORTED.
  */
 int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_params,
                    void* v_codes, void* v_params, const int32_t* cache_seqlens,
@@ -383,7 +385,8 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
  *                row j over the query heads of kv head h, for j < kv_seqlens[b], and 0
  *                for the rows after them
  *   weights_in   the same layout, may be weights_out itself; NULL counts as zeros
- * Any group size Hq / Hkv.  ALiBi as in mea_decode (position = row number).  An empty
+ * Any group size Hq / Hkv.  ALiBi as in mea_decode (position = row number; rows that
+ * mea_cache_evict has moved count from where they are now).  An empty
  * sequence gives out = 0, lse = -inf.  A sequence whose length is negative or above
  * min(max_kv_len, cache_rows) gets out = 0 and lse = NaN, its weights_out is left as
  * it was, and the device status word records MEA_ERR_INVALID_ARG.
@@ -410,7 +413,7 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
  *   q    [B, M, Hq, K], k [B, N, Hkv, K]  element strides (b, row, h), K contiguous
  *   lse  [B, Hq, M] fp32 natural log, as written by mea_fwd (bias none or causal) or
  *        mea_prefill_chunk for the same q, scale and alibi; a row with lse = -inf adds
- *        nothing
+ *        nothing, a NaN (or a NaN in q or k) makes the weights it touches NaN
  *   cache_seqlens, q_seqlens  DEVICE int32 [B] as given to mea_prefill_chunk (the rows
  *        before the chunk, and the chunk's real rows, M if NULL): row i sits at position
  *        past + i and key rows [0, past + n) take part.  cache_seqlens NULL: all N keys
@@ -421,8 +424,7 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
  * A sequence with past < 0, n outside [0, M] or past + n > N is skipped (weights_out
  * left as it was) and records MEA_ERR_INVALID_ARG in the device status word; a bounded
  * wait that gives up records MEA_ERR_DEVICE_TIMEOUT and leaves NaN in its keys' weights.
- * The same call gives the same bits every time.  scale must be >= 0 and K 64 or 128;
- * for M = 0 pass cache_seqlens.
+ * The same call gives the same bits every time.  M >= 1, scale >= 0, K 64 or 128.
  */
 int mea_key_weights(const void* q, const void* k, const float* lse, const int32_t* cache_seqlens,
                     const int32_t* q_seqlens, const float* weights_in, float* weights_out, int B,

@@ -21,6 +21,7 @@ bool strides_ok(const int64_t s[3]) {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int kMaxLen = 1 << 30;  // rows of one sequence: tile arithmetic stays in 32 bits
 
 // False if the batch has 2^31 rows or more.
 bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
@@ -72,6 +73,7 @@ int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_
   if (!k_new || !v_new || !k_codes || !k_params || !v_codes || !v_params || !cache_seqlens)
     return MEA_ERR_INVALID_ARG;
   if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  if (M > kMaxLen || cache_rows > kMaxLen) return MEA_ERR_UNSUPPORTED;
   for (const void* p : {k_new, v_new, static_cast<const void*>(k_codes),
                         static_cast<const void*>(k_params), static_cast<const void*>(v_codes),
                         static_cast<const void*>(v_params)})
@@ -112,6 +114,7 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
   if (!k_codes || !k_params || !v_codes || !v_params || !rows || !k_out || !v_out)
     return MEA_ERR_INVALID_ARG;
   if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  if (out_rows > kMaxLen || cache_rows > kMaxLen) return MEA_ERR_UNSUPPORTED;
   for (const void* p : {k_codes, k_params, v_codes, v_params, static_cast<const void*>(k_out),
                         static_cast<const void*>(v_out)})
     if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
@@ -178,6 +181,7 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
   if (cache_rows > 0 && (!k_codes || !k_params || !v_codes || !v_params))
     return MEA_ERR_INVALID_ARG;
   if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
+  if (cache_rows > kMaxLen || max_kv_len > kMaxLen) return MEA_ERR_UNSUPPORTED;
   for (const void* p : {q, k_codes, k_params, v_codes, v_params, static_cast<const void*>(out)})
     if (!aligned16(p)) return MEA_ERR_UNSUPPORTED;
   size_t lse_at, score_at;
@@ -244,7 +248,7 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
   if (M < 1) return MEA_ERR_INVALID_ARG;
   if (!q || !k || !lse || !weights_out) return MEA_ERR_INVALID_ARG;
   if (K != 64 && K != 128) return MEA_ERR_UNSUPPORTED;
-  if (scale < 0.f) return MEA_ERR_UNSUPPORTED;
+  if (scale < 0.f || M > kMaxLen || N > kMaxLen) return MEA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k)) return MEA_ERR_UNSUPPORTED;
   if (!strides_ok(q_strides) || !strides_ok(k_strides)) return MEA_ERR_UNSUPPORTED;
   const int64_t blocks = (static_cast<int64_t>(N) + mea::kWeightKeys - 1) / mea::kWeightKeys;
@@ -308,7 +312,8 @@ int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weight
   if (!cache_seqlens || !new_seqlens || cache_seqlens == new_seqlens || !kept || !weights_out ||
       !weights || cache_rows < 1)
     return MEA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * Hkv > 65535) return MEA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * Hkv > 65535 || cache_rows > kMaxLen || out_rows > kMaxLen)
+    return MEA_ERR_UNSUPPORTED;
 
   mea_plane_t all[mea::kMaxPlanes];
   for (int p = 0; p < n_planes; ++p) all[p] = planes[p];
@@ -333,6 +338,7 @@ int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weight
                    static_cast<int64_t>(reinterpret_cast<uintptr_t>(x.dst) & 15u);
     for (int i = 0; i < 3; ++i) {
       if (x.src_strides[i] < 0 || x.dst_strides[i] < 0) return MEA_ERR_INVALID_ARG;
+      if ((x.src_strides[i] | x.dst_strides[i]) >= (int64_t(1) << 40)) return MEA_ERR_UNSUPPORTED;
       bits |= x.src_strides[i] | x.dst_strides[i];
     }
     if (bits & 3) return MEA_ERR_UNSUPPORTED;

@@ -182,6 +182,61 @@ def test_bad_lengths_are_reported(mea):
         assert all(torch.equal(a, b) for a, b in zip(src, before))
 
 
+def test_graph_and_stream(mea):
+    """Captured eviction replayed on other weights and lengths; another stream."""
+    src = tuple(t.to(DEV) for t in make(False, 2, 400, 2, 64, 7))
+    dst = tuple(torch.zeros_like(t[:, :60]) for t in src)
+    w, n = torch.zeros(2, 2, 400, device=DEV), i32([400, 400])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        new, kept, wo = mea.mea_cache_evict(src, w, n, 50, 9, out=dst)
+    for seed, lens in ((1, [400, 77]), (2, [20, 399])):
+        w.copy_(weights("ties", 2, 2, 400, seed))
+        n.copy_(i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert new.tolist() == [min(x, 50) for x in lens]
+        for b in range(2):
+            for h in range(2):
+                rows = U.choose(w[b, h].cpu(), lens[b], 50, 9)
+                assert kept[b, h, :len(rows)].tolist() == rows
+                assert torch.equal(dst[0][b, :len(rows), h], src[0][b, rows, h])
+                assert torch.equal(wo[b, h, :len(rows)], w[b, h, rows])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    new2, kept2, wo2 = mea.mea_cache_evict(src, w, n, 50, 9, stream=side,
+                                           out=tuple(torch.zeros_like(t) for t in dst))
+    side.synchronize()
+    assert torch.equal(kept, kept2) and torch.equal(wo, wo2) and torch.equal(new, new2)
+
+
+def test_two_streams_at_once(mea):
+    """Calls on two streams with buffers of their own, interleaved, give what they give alone."""
+    a = mea.mea_kv4_alloc(2, 700, 2, 128, torch.bfloat16, DEV)
+    b = mea.mea_kv4_alloc(2, 700, 2, 128, torch.bfloat16, DEV)
+    x = torch.randn(2, 700, 2, 128, generator=gen(1)).bfloat16().to(DEV)
+    q = torch.randn(2, 8, 128, generator=gen(2)).bfloat16().to(DEV)
+    for c in (a, b):
+        mea.mea_kv4_append(x, x, c, i32([0, 0]))
+    n, w = i32([700, 600]), weights("random", 2, 2, 700, 3).to(DEV)
+    want = mea.mea_decode_kv4(q, a, n, 700, weights=w, return_weights=True)
+    out = mea.mea_kv4_alloc(2, 300, 2, 128, torch.bfloat16, DEV)
+    _, kept, _ = mea.mea_cache_evict(a, want[2], n, 300, 30, out=out)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [mea.mea_kv4_alloc(2, 300, 2, 128, torch.bfloat16, DEV) for _ in streams]
+    for _ in range(5):
+        got = []
+        for s, c, o in zip(streams, (a, b), outs):
+            with torch.cuda.stream(s):
+                r = mea.mea_decode_kv4(q, c, n, 700, weights=w, return_weights=True)
+                got.append((r, mea.mea_cache_evict(c, r[2], n, 300, 30, out=o)[1]))
+        torch.cuda.synchronize()
+        for (r, k), o in zip(got, outs):
+            assert all(torch.equal(x, y) for x, y in zip(r, want)) and torch.equal(k, kept)
+            assert all(torch.equal(x, y) for x, y in zip(o, out))
+
+
 def test_serving_run(mea):
     """Prompt into the 4-bit cache, its keys weighed, cut to the budget, decode steps that
     keep weighing, cut again in place, decode: every step against the plain forms."""

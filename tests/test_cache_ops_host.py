@@ -39,7 +39,8 @@ WEIGH = dict(q=P(4096), k=P(4096), lse=P(16), clen=None, qlen=None, win=None, wo
     (dict(k=None), INVALID), (dict(vp=None), INVALID), (dict(lens=None), INVALID),
     (dict(K=96), UNSUPPORTED), (dict(k=P(4104)), UNSUPPORTED), (dict(kp=P(4100)), UNSUPPORTED),
     (dict(ks=I64(1024, 60, 64)), UNSUPPORTED), (dict(vs=I64(1024, 0, 64)), UNSUPPORTED),
-    (dict(B=1 << 16, M=1 << 16), UNSUPPORTED), (dict(B=0), OK), (dict(M=0), OK)])
+    (dict(B=1 << 16, M=1 << 16), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED),
+    (dict(B=0), OK), (dict(M=0), OK)])
 def test_append(kw, code):
     assert call(m.lib.mea_kv4_append, APPEND, **kw) == code
 
@@ -49,7 +50,8 @@ def test_append(kw, code):
     (dict(dtype=-1), INVALID), (dict(ks=None), INVALID), (dict(kc=None), INVALID),
     (dict(rows_t=None), INVALID), (dict(v=None), INVALID), (dict(K=32), UNSUPPORTED),
     (dict(v=P(4098)), UNSUPPORTED), (dict(vs=I64(1024, 64, -64)), UNSUPPORTED),
-    (dict(B=1 << 16, out=1 << 16), UNSUPPORTED), (dict(B=0), OK), (dict(out=0), OK)])
+    (dict(B=1 << 16, out=1 << 16), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED),
+    (dict(B=0), OK), (dict(out=0), OK)])
 def test_read(kw, code):
     assert call(m.lib.mea_kv4_read, READ, **kw) == code
 
@@ -62,7 +64,8 @@ def test_read(kw, code):
     (dict(q=P(4104)), UNSUPPORTED), (dict(vc=P(4104)), UNSUPPORTED),
     (dict(B=70000), UNSUPPORTED), (dict(bound=4000, bytes=16), WORKSPACE),
     (dict(bound=4000, ws=None), WORKSPACE), (dict(bound=4000, ws=P(4112)), WORKSPACE),
-    (dict(wout=P(16), ws=None), WORKSPACE), (dict(B=0), OK)])
+    (dict(wout=P(16), ws=None), WORKSPACE), (dict(bound=(1 << 30) + 1), UNSUPPORTED),
+    (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(B=0), OK)])
 def test_decode(kw, code):
     if kw.get("B") == 70000:
         kw = dict(kw, bound=10)
@@ -76,7 +79,8 @@ def test_decode(kw, code):
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(lse=None), INVALID),
     (dict(wout=None), INVALID), (dict(qs=None), INVALID), (dict(scale=-1.0), UNSUPPORTED),
     (dict(K=80), UNSUPPORTED), (dict(k=P(4104)), UNSUPPORTED),
-    (dict(ks=I64(1024, 65, 64)), UNSUPPORTED), (dict(B=0), OK), (dict(N=0), OK)])
+    (dict(ks=I64(1024, 65, 64)), UNSUPPORTED), (dict(N=(1 << 30) + 1), UNSUPPORTED),
+    (dict(B=0), OK), (dict(N=0), OK)])
 def test_key_weights(kw, code):
     assert call(m.lib.mea_key_weights, WEIGH, **kw) == code
 
@@ -102,6 +106,7 @@ def evict(plane=None, n=1, w=P(1 << 20), wo=P(2 << 20), lens=P(16), new=P(64), k
     (dict(row_bytes=0), INVALID), (dict(src_strides=I64(-320, 32, 16)), INVALID),
     (dict(row_bytes=6), UNSUPPORTED), (dict(src=(1 << 24) + 2), UNSUPPORTED),
     (dict(dst_strides=I64(192, 34, 16)), UNSUPPORTED), (dict(B=40000), UNSUPPORTED),
+    (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(src_strides=I64(1 << 41, 32, 16)), UNSUPPORTED),
     (dict(dst=1 << 24), INVALID),                      # in place, but fewer rows
     (dict(dst=(1 << 24) + 320), INVALID),              # overlaps its source
     (dict(dst=1 << 20), INVALID),                      # overlaps the weights
