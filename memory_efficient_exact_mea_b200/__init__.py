@@ -465,25 +465,32 @@ def _cuda_index(t, name):
     return index
 
 
-def _on(index, **tensors):
-    """Every tensor given lies on CUDA device `index`."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+def _elsewhere(name, index):
+    return ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
 
 
-def _lens(B, index, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or t.get_device() != index
-                              or t.shape != (B,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of B entries on "
-                             f"cuda:{index}")
+def _on(index, t, name):
+    """t, if given, lies on CUDA device `index`."""
+    if t is not None and t.get_device() != index:
+        raise _elsewhere(name, index)
 
 
-def _weights_tensor(t, shape, name):
-    if t is not None and (t.dtype != torch.float32 or t.shape != shape
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
+def _lens(B, index, t, name):
+    """t, if given, is one int32 a sequence on CUDA device `index`."""
+    if t is not None and (t.dtype is not _I32 or t.get_device() != index or t.dim() != 1
+                          or t.numel() != B or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of B entries on cuda:{index}")
+
+
+def _f32(t, shape, index, name):
+    """t, if given, is a contiguous float32 tensor of `shape` on CUDA device `index`."""
+    if t is not None and (t.dtype is not _F32 or t.shape != shape or t.get_device() != index
                           or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
+        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor on "
+                         f"cuda:{index}")
 
 
 class Kv4Cache(NamedTuple):
@@ -515,13 +522,13 @@ def _kv4_dims(cache: Kv4Cache, what="cache"):
     """(B, Hkv, rows, K, dtype, device index) of a 4-bit cache, checked."""
     kc, kp, vc, vp = cache
     shape = kc.shape
-    if len(shape) != 4 or kc.dtype != torch.uint8:
+    if len(shape) != 4 or kc.dtype is not _U8:
         raise ValueError(f"{what}: codes must be uint8 [B, Hkv, rows, K/2]")
     B, Hkv, rows, half = shape
     dtype = kp.dtype
     if dtype not in _DTYPE or vp.dtype != dtype:
         raise ValueError(f"{what}: params must share dtype float16 or bfloat16")
-    if vc.dtype != torch.uint8 or vc.shape != shape:
+    if vc.dtype is not _U8 or vc.shape != shape:
         raise ValueError(f"{what}: k_codes and v_codes must be alike")
     want = (B, Hkv, rows, half // 32, 2)
     if half % 32 or kp.shape != want or vp.shape != want:
@@ -547,8 +554,10 @@ def mea_kv4_append(k_new, v_new, cache: Kv4Cache, cache_seqlens, q_seqlens=None,
         raise ValueError("k_new and v_new must be [B, M, Hkv, K]")
     if k_new.dtype != dtype or v_new.dtype != dtype:
         raise ValueError("k_new and v_new must have the dtype of the cache's params")
-    _on(index, k_new=k_new, v_new=v_new)
-    _lens(B, index, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    _on(index, k_new, "k_new")
+    _on(index, v_new, "v_new")
+    _lens(B, index, cache_seqlens, "cache_seqlens")
+    _lens(B, index, q_seqlens, "q_seqlens")
     kc, kp, vc, vp = cache
     _launch("mea_kv4_append", lib.mea_kv4_append, index, stream, (),
             (k_new.data_ptr(), v_new.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(),
@@ -577,8 +586,10 @@ def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
     if k_out.shape != shape or v_out.shape != shape or k_out.dtype != dtype \
             or v_out.dtype != dtype:
         raise ValueError(f"k_out and v_out must be {list(shape)} of the params' dtype")
-    _on(index, k_out=k_out, v_out=v_out)
-    _lens(B, index, rows=rows, first_rows=first_rows)
+    _on(index, k_out, "k_out")
+    _on(index, v_out, "v_out")
+    _lens(B, index, rows, "rows")
+    _lens(B, index, first_rows, "first_rows")
     kc, kp, vc, vp = cache
     _launch("mea_kv4_read", lib.mea_kv4_read, index, stream, fresh,
             (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), rows.data_ptr(),
@@ -622,22 +633,23 @@ def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float
     elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped and typed like q")
     if lse is not None:
-        _weights_tensor(lse, (B, Hq), "lse")
+        _f32(lse, (B, Hq), index, "lse")
     elif return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
         fresh.append(lse)
     want = return_weights or weights_out is not None
     if weights is not None and not want:
         raise ValueError("weights needs return_weights or weights_out")
     if want:
         if weights_out is None:
-            weights_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=q.device)
+            weights_out = torch.empty((B, Hkv, cap), dtype=_F32, device=q.device)
             fresh.append(weights_out)
-        _weights_tensor(weights, (B, Hkv, cap), "weights")
-        _weights_tensor(weights_out, (B, Hkv, cap), "weights_out")
-    _on(index, q=q, out=out, lse=lse, weights=weights, weights_out=weights_out,
-        workspace=workspace)
-    _lens(B, index, kv_seqlens=kv_seqlens)
+        _f32(weights, (B, Hkv, cap), index, "weights")
+        _f32(weights_out, (B, Hkv, cap), index, "weights_out")
+    _on(index, q, "q")
+    _on(index, out, "out")
+    _on(index, workspace, "workspace")
+    _lens(B, index, kv_seqlens, "kv_seqlens")
     ws_bytes = 0
     if workspace is None:
         need = mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, want)
@@ -678,23 +690,29 @@ def mea_key_weights(q, k, lse, cache_seqlens=None, q_seqlens=None, causal: bool 
         raise ValueError("q_seqlens needs cache_seqlens")
     if lse is None:
         raise ValueError("lse must be what the attention of these queries returned")
-    _weights_tensor(lse, (B, Hq, M), "lse")
     scale = K ** -0.5 if scale is None else float(scale)
+    index = _cuda_index(q, "q")
     fresh = []
     if out is None:
-        out = torch.empty((B, Hkv, N), dtype=torch.float32, device=q.device)
+        out = torch.empty((B, Hkv, N), dtype=_F32, device=q.device)
         fresh.append(out)
-    _weights_tensor(weights, (B, Hkv, N), "weights")
-    _weights_tensor(out, (B, Hkv, N), "out")
-    index = _cuda_index(q, "q")
-    _on(index, k=k, lse=lse, weights=weights, out=out)
-    _lens(B, index, cache_seqlens=cache_seqlens, q_seqlens=q_seqlens)
+    _f32(lse, (B, Hq, M), index, "lse")
+    _f32(weights, (B, Hkv, N), index, "weights")
+    _f32(out, (B, Hkv, N), index, "out")
+    _on(index, k, "k")
+    _lens(B, index, cache_seqlens, "cache_seqlens")
+    _lens(B, index, q_seqlens, "q_seqlens")
     _launch("mea_key_weights", lib.mea_key_weights, index, stream, fresh,
             (q.data_ptr(), k.data_ptr(), lse.data_ptr(), _addr(cache_seqlens), _addr(q_seqlens),
              _addr(weights), out.data_ptr(), B, M, N, Hq, Hkv, K, _bmhk_strides(q, "q"),
              _bmhk_strides(k, "k"), _DTYPE[q.dtype], 1 if causal else 0, 1 if alibi else 0,
              scale))
     return out
+
+
+def _byte_strides(st, size, r, h):
+    """ctypes int64[3] of a tensor's (b, row, head) strides in bytes."""
+    return _i64x3(st[0] * size, st[r] * size, st[h] * size)
 
 
 def _planes_of(cache, what):
@@ -712,7 +730,7 @@ def _planes_of(cache, what):
     if k.shape[:3] != v.shape[:3]:
         raise ValueError(f"{what}: k and v must have the same rows and heads")
     index = _cuda_index(k, what)
-    _on(index, v=v)
+    _on(index, v, f"{what}: v")
     return [(k, (1, 2)), (v, (1, 2))], k.shape[0], k.shape[2], k.shape[1], index
 
 
@@ -750,21 +768,22 @@ def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out
     if kept is None:
         kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
         fresh.append(kept)
-    _weights_tensor(weights, (B, Hkv, rows), "weights")
-    _weights_tensor(weights_out, (B, Hkv, out_rows), "weights_out")
-    if kept.dtype != torch.int32 or kept.shape != (B, Hkv, budget) or not kept.is_contiguous():
+    _f32(weights, (B, Hkv, rows), index, "weights")
+    _f32(weights_out, (B, Hkv, out_rows), index, "weights_out")
+    if kept.dtype is not _I32 or kept.shape != (B, Hkv, budget) or not kept.is_contiguous():
         raise ValueError("kept must be a contiguous int32 [B, Hkv, budget] tensor")
-    _on(index, weights=weights, weights_out=weights_out, kept=kept)
-    _lens(B, index, cache_seqlens=cache_seqlens, new_seqlens=new_seqlens)
+    _on(index, kept, "kept")
+    _lens(B, index, cache_seqlens, "cache_seqlens")
+    _lens(B, index, new_seqlens, "new_seqlens")
     planes = (_Plane * len(src))()
-    for p, ((s, (r, h)), (d, _)) in enumerate(zip(src, dst)):
-        if s.dtype != d.dtype or s.shape[3:] != d.shape[3:]:
+    for plane, (s, (r, h)), (d, _) in zip(planes, src, dst):
+        if s.dtype is not d.dtype or s.shape[3:] != d.shape[3:]:
             raise ValueError("out must have the rows of the cache")
-        size, ss, ds = s.element_size(), s.stride(), d.stride()
-        planes[p] = _Plane(s.data_ptr(), d.data_ptr(),
-                           _i64x3(ss[0] * size, ss[r] * size, ss[h] * size),
-                           _i64x3(ds[0] * size, ds[r] * size, ds[h] * size),
-                           s.shape[3:].numel() * size)
+        size = s.element_size()
+        plane.src, plane.dst = s.data_ptr(), d.data_ptr()
+        plane.src_strides = _byte_strides(s.stride(), size, r, h)
+        plane.dst_strides = plane.src_strides if d is s else _byte_strides(d.stride(), size, r, h)
+        plane.row_bytes = s.shape[3:].numel() * size
     _launch("mea_cache_evict", lib.mea_cache_evict, index, stream, fresh,
             (planes, len(src), weights.data_ptr(), weights_out.data_ptr(),
              cache_seqlens.data_ptr(), new_seqlens.data_ptr(), kept.data_ptr(), B, Hkv, rows,

@@ -125,15 +125,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
 
   // Rows above the key `prefix` are kept, and the first `need` equal to it.
-  uint32_t base = 0;  // rows so far: above in the low half-word counts, equal kept apart
-  uint32_t base_eq = 0;
-#pragma unroll 1
-  for (int t0 = 0; t0 < m; t0 += kSelTile) {
+  uint32_t base = 0, base_eq = 0;  // rows before this tile: above, and equal
+  auto place = [&](int t0, const uint32_t(&keys)[4]) {
     uint32_t gt[4], eq[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = t0 + u * kSelThreads + tid;
-      const uint32_t key = j < m ? order_key(w[j]) : 0u;
+      const uint32_t key = keys[u];
       gt[u] = __ballot_sync(0xffffffffu, j < m && key > prefix);
       eq[u] = __ballot_sync(0xffffffffu, j < m && key == prefix);
       if (lane == 0) counts[u * 32 + warp] = __popc(gt[u]) | (__popc(eq[u]) << 16);
@@ -170,6 +168,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     base += warp_sum[0] & 0xffffu;
     base_eq += warp_sum[0] >> 16;
     __syncthreads();
+  };
+  static_assert(kSelHeld == 8, "two tiles are held");
+  if (held) {
+    place(0, {mine[0], mine[1], mine[2], mine[3]});
+    if (m > kSelTile) place(kSelTile, {mine[4], mine[5], mine[6], mine[7]});
+  } else {
+#pragma unroll 1
+    for (int t0 = 0; t0 < m; t0 += kSelTile) {
+      uint32_t keys[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = t0 + u * kSelThreads + tid;
+        keys[u] = j < m ? order_key(w[j]) : 0u;
+      }
+      place(t0, keys);
+    }
   }
 }
 

@@ -118,7 +118,7 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 5) kv4_append_kernel(const Kv4AppendArgs a) {
   constexpr int kLanes = D / 8;  // lanes per row
   const unsigned group =
       blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;  // of kRowGroup rows
