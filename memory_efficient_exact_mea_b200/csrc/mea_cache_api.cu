@@ -51,7 +51,7 @@ DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
   const int64_t units = static_cast<int64_t>(B) * Hkv * p.head_blocks;
   const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
   int64_t chunk = (max_len + want - 1) / want;
-  chunk = std::min<int64_t>(2048, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  chunk = std::min<int64_t>(1536, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);
   return p;

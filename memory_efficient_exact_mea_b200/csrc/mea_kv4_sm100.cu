@@ -343,6 +343,11 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // rows: one byte permute joins the halves of the two rows' words.  Each warp copies
 // its own tiles into a ring of its own (cp.async, 16-byte chunks, no barrier but
 // __syncwarp), two tiles ahead.
+//
+// PAIR (K = 128, at most four heads): the columns that would be padding take the
+// second group of dimensions, so a thread works for one group only -- half the
+// arithmetic between the products (scores, p s, sums), one exchange of the scores'
+// halves.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -427,21 +432,26 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     return (r >> 2) * 128 + (((((r & 3) << 1) | c) ^ (((r >> 2) & 1) << 1)) << 4);
 }
 
-template <int D, bool BF16, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4DecodeArgs a) {
+template <int D, bool BF16, bool ALIBI, bool PAIR>
+__global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = KSmem<D>;
   constexpr int NG = L::NG;  // groups of a row
+  static_assert(!PAIR || NG == 2, "a column for each group and head");
+  constexpr int NT = PAIR ? 1 : NG;  // groups a thread's columns stand for
   extern __shared__ __align__(128) uint8_t smem[];
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int kvh = blockIdx.y / a.head_blocks;
-  const int g0 = (blockIdx.y - kvh * a.head_blocks) * kHeads;  // first head within the group
+  // The split varies slowest: whole chunks start first, the ragged last ones fill the end.
+  const int split = blockIdx.z, b = blockIdx.y;
+  const int kvh = blockIdx.x / a.head_blocks;
+  const int g0 = (blockIdx.x - kvh * a.head_blocks) * kHeads;  // first head within the group
   const int heads = min(kHeads, a.group - g0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
+  // columns 2 tig, 2 tig + 1 of a product: heads hp, hp + 1 (of the thread's group)
+  const int own = PAIR ? tig >> 1 : 0, hp = PAIR ? 2 * (tig & 1) : 2 * tig;
   const int n = a.kv_lens[b];
   const int h0 = kvh * a.group + g0;
   const bool ok = n >= 0 && n <= a.max_len;
-  if (!ok && split == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+  if (!ok && split == 0 && blockIdx.x == 0 && threadIdx.x == 0)
     record_error(a.status, kErrInvalidArg);
   if (!ok || n == 0) {
     if (a.part_o == nullptr) {  // no merge follows
@@ -512,20 +522,22 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
   }
 
   // Q^T as the B operand (head gid), scaled; the sums of q that go with the zeros,
-  // for this thread's two heads (2 tig, 2 tig + 1).
+  // for this thread's two columns.  Column gid is head gid, or (PAIR) head gid % 4 with
+  // the dimensions of group gid / 4 alone.
   uint32_t qb[NG][4][2];
-  float qsum[NG][2], scl[2];
+  float qsum[NT][2], scl[2];
   {
+    const int head = PAIR ? gid & 3 : gid;
     const uint4* qrow = reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(a.q) +
-        (static_cast<long long>(b) * a.Hq + h0 + (gid < heads ? gid : 0)) * D + 16 * tig);
+        (static_cast<long long>(b) * a.Hq + h0 + (head < heads ? head : 0)) * D + 16 * tig);
     uint32_t big2 = 0u;  // largest magnitudes, as pairs of bit patterns
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint4 x = qrow[8 * g + w];  // dimensions 64 g + 16 tig + 8 w + 0..7
-        if (gid >= heads) x = make_uint4(0, 0, 0, 0);
+        if (head >= heads) x = make_uint4(0, 0, 0, 0);
         big2 = __vmaxu2(__vmaxu2(big2, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
         qb[g][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);  // pairs (d, d + 4)
@@ -543,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     if (!BF16 && big != 0u && big < 0x7c00u) k = min(22 - static_cast<int>(big >> 10), 15);
     k = min(max(k, -126), 126);
     const float f = __int_as_float((127 + k) << 23), inv = __int_as_float((127 - k) << 23);
+    float col_sum = 0.f;  // PAIR: of the column's own group
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float sum = 0.f;
@@ -558,11 +571,19 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
           sum += __low2float(x) + __high2float(x);
           if (e == 0) x = __hmul2(x, __float2half2_rn(kUnitEven / kUnitOdd));
           qb[g][ks][e] = *reinterpret_cast<const uint32_t*>(&x);
+          if (PAIR && (gid >> 2) != g) qb[g][ks][e] = 0u;
         }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (PAIR && (gid >> 2) == g) col_sum = sum;
+      if constexpr (!PAIR) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) qsum[g][e] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * e);
+        for (int e = 0; e < 2; ++e) qsum[g][e] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * e);
+      }
+    }
+    if constexpr (PAIR) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qsum[0][e] = __shfl_sync(0xffffffffu, col_sum, 8 * tig + 4 * e);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -572,15 +593,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
   if constexpr (ALIBI) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      slope[e] = exp2f(-8.0f * static_cast<float>(h0 + 2 * tig + e + 1) / a.Hq) * kLog2e;
+      slope[e] = exp2f(-8.0f * static_cast<float>(h0 + hp + e + 1) / a.Hq) * kLog2e;
   }
 
   float ref[2] = {kNoRef, kNoRef}, l_part[2] = {0.f, 0.f};
-  float zacc[NG][2], acc[D / 16][4];
+  float zacc[NT][2], acc[D / 16][4];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    zacc[g][0] = zacc[g][1] = 0.f;
-  }
+  for (int g = 0; g < NT; ++g) zacc[g][0] = zacc[g][1] = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -589,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
   // Scores of the tile in `slot` times the scale of q.
   auto score = [&](int slot, float(&y)[2][4]) {
     const uint8_t* st = ring + slot * L::kStage;
-    float sc[2][NG][4];
+    float sc[2][NT][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       uint32_t kw[4][2];
@@ -606,26 +625,25 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
           for (int blk = 0; blk < 2; ++blk) {
             const CodePairs &lo = c[2 * blk], &hi = c[2 * blk + 1];
             const uint32_t(&q2)[2] = qb[g][2 * w + half];
-            if (w + half == 0)
-              mma_f16(sc[blk][g], lo.n[0], hi.n[0], lo.n[1], hi.n[1], q2[0], q2[1], 0.f, 0.f, 0.f,
-                      0.f);
+            float(&s4)[4] = sc[blk][PAIR ? 0 : g];
+            if (w + half == 0 && (!PAIR || g == 0))
+              mma_f16(s4, lo.n[0], hi.n[0], lo.n[1], hi.n[1], q2[0], q2[1], 0.f, 0.f, 0.f, 0.f);
             else
-              mma_f16_acc(sc[blk][g], lo.n[2 * half], hi.n[2 * half], lo.n[2 * half + 1],
+              mma_f16_acc(s4, lo.n[2 * half], hi.n[2 * half], lo.n[2 * half + 1],
                           hi.n[2 * half + 1], q2[0], q2[1]);
           }
       }
     }
-    uint32_t kq[4][NG];
+    uint32_t kq[4][NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lds<4 * NG>(st + 2 * L::kCodes + (gid + 8 * i) * 4 * NG, kq[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+      lds<4 * NT>(st + 2 * L::kCodes + (gid + 8 * i) * 4 * NG + 4 * own, kq[i]);
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NT; ++g) {
           const float s = step_of<BF16>(kq[2 * blk + r][g]) * kUnitOdd;
           const float z = zero_of<BF16>(kq[2 * blk + r][g]);
 #pragma unroll
@@ -634,6 +652,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
             yy = fmaf(s, sc[blk][g][2 * r + e], g == 0 ? z * qsum[g][e] : fmaf(z, qsum[g][e], yy));
           }
         }
+    }
+    if constexpr (PAIR) {  // the other group's share, two columns of tig on
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[blk][e] += __shfl_xor_sync(0xffffffffu, y[blk][e], 2);
     }
   };
 
@@ -646,10 +670,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     float y[2][4];
     score(slot, y);
     slot = slot == kStages - 1 ? 0 : slot + 1;
-    uint32_t vq[4][NG];  // (s, z) of the V rows gid + 8 i
+    uint32_t vq[4][NT];  // (s, z) of the V rows gid + 8 i
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds<4 * NG>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG, vq[i]);
+      lds<4 * NT>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG + 4 * own, vq[i]);
     const bool last = t + kTile > s1;
     if constexpr (ALIBI) {
       // y scl - slope (n - 1 - row): y carries the bias in its own units
@@ -667,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     if (a.scores != nullptr) {  // kept for the gathered weights
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (2 * tig + e < heads) {
-          float* out = a.scores + (static_cast<long long>(b) * a.Hq + h0 + 2 * tig + e) *
+        if (own == 0 && hp + e < heads) {
+          float* out = a.scores + (static_cast<long long>(b) * a.Hq + h0 + hp + e) *
                                       a.score_stride + t + gid;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -678,14 +702,14 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     // Weights of the tile against the present reference: p s in fp16, and the sums
     // of p, p s and p z (an overflow shows in a sum of numbers >= 0).
     constexpr int kParts = BF16 ? 1 : 2;
-    uint32_t pk[2][NG][2][kParts];
-    float sum[2], heavy[2], zsum[NG][2];
+    uint32_t pk[2][NT][2][kParts];
+    float sum[2], heavy[2], zsum[NT][2];
     auto weigh = [&] {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         sum[e] = heavy[e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) zsum[g][e] = 0.f;
+        for (int g = 0; g < NT; ++g) zsum[g][e] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // row gid + 8 i
@@ -698,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
           if (t + 8 * i + gid >= s1) p[0] = p[1] = 0.f;
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NT; ++g) {
           const float s = step_of<BF16>(vq[i][g]), z = zero_of<BF16>(vq[i][g]);
           const float ps0 = p[0] * s, ps1 = p[1] * s;
           heavy[0] += ps0;
@@ -728,11 +752,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
         for (int i = 0; i < 4; ++i) {
           float mag = 0x1p-60f;
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
+          for (int g = 0; g < NT; ++g)
             mag = fmaxf(mag, fmaxf(step_of<BF16>(vq[i][g]),
                                    fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f));
           v = fmaxf(v, y[i >> 1][2 * (i & 1) + e] * unit[e] + rintf(__log2f(mag)));
         }
+        if constexpr (PAIR) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -741,9 +766,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
         ref[e] = r_new;
         l_part[e] *= alpha;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          zacc[g][e] *= alpha;
-        }
+        for (int g = 0; g < NT; ++g) zacc[g][e] *= alpha;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           acc[i][e] *= alpha;
@@ -755,17 +778,26 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     l_part[0] += sum[0];
     l_part[1] += sum[1];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < NT; ++g) {
       zacc[g][0] += zsum[g][0];
       zacc[g][1] += zsum[g][1];
+    }
+    uint32_t pb[2][NT][kParts][2];
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        uint32_t pb[kParts][2];
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int g = 0; g < NT; ++g)
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
-          pb[part][0] = movmatrix_trans(pk[blk][g][0][part]);
-          pb[part][1] = movmatrix_trans(pk[blk][g][1][part]);
+          pb[blk][g][part][0] = movmatrix_trans(pk[blk][g][0][part]);
+          pb[blk][g][part][1] = movmatrix_trans(pk[blk][g][1][part]);
         }
+    // PAIR: a group's dimensions against all columns; those of the other group are
+    // computed for nothing (they were the padding) and left out in the end
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
         // rows 2 tig, 2 tig + 1 (first pair) and + 8 (second): words of 8 dimensions
         uint32_t w0, w1, w2, w3;
         lds<4>(st + v_at[0][g] + blk * 8 * D, &w0);
@@ -780,8 +812,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
-            mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[part][0],
-                        pb[part][1]);
+            mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i],
+                        pb[blk][PAIR ? 0 : g][part][0], pb[blk][PAIR ? 0 : g][part][1]);
       }
     }
   }
@@ -792,27 +824,28 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_kernel(const Kv4Decode
     for (int o = 4; o <= 16; o <<= 1) {
       l_part[e] += __shfl_xor_sync(0xffffffffu, l_part[e], o);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) zacc[g][e] += __shfl_xor_sync(0xffffffffu, zacc[g][e], o);
+      for (int g = 0; g < NT; ++g) zacc[g][e] += __shfl_xor_sync(0xffffffffu, zacc[g][e], o);
     }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();  // the rings are read: their memory joins the warps' states
   float* c_ref = reinterpret_cast<float*>(smem);
   float* c_l = c_ref + kWarps * kHeads;
   float* c_acc = c_l + kWarps * kHeads;
-  if (gid == 0) {
+  if (gid == 0 && own == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      c_ref[warp * kHeads + 2 * tig + e] = ref[e];
-      c_l[warp * kHeads + 2 * tig + e] = l_part[e];
+      c_ref[warp * kHeads + hp + e] = ref[e];
+      c_l[warp * kHeads + hp + e] = l_part[e];
     }
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e)  // tile i: dimension 64 (i/4) + 8 gid + i % 4 (+ 4)
-      c_acc[(warp * kHeads + 2 * tig + (e & 1)) * D + 64 * (i >> 2) + 8 * gid + (i & 3) +
-            4 * (e >> 1)] =
-          fmaf(acc[i][e], (i & 1) ? kUnitOdd : kUnitEven, zacc[i >> 2][e & 1]);
+      if (!PAIR || own == (i >> 2))
+        c_acc[(warp * kHeads + hp + (e & 1)) * D + 64 * (i >> 2) + 8 * gid + (i & 3) +
+              4 * (e >> 1)] =
+            fmaf(acc[i][e], (i & 1) ? kUnitOdd : kUnitEven, zacc[PAIR ? 0 : i >> 2][e & 1]);
   __syncthreads();
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
@@ -953,18 +986,27 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
   }
 }
 
+template <int D, bool BF16, bool ALIBI, bool PAIR>
+cudaError_t decode_run(const Kv4DecodeArgs& a, dim3 grid, cudaStream_t stream) {
+  constexpr auto kern = kv4_decode_kernel<D, BF16, ALIBI, PAIR>;
+  const cudaError_t e = set_smem_once<kern>(KSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, KSmem<D>::kBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <int D, bool BF16>
 cudaError_t decode_t(const Kv4DecodeArgs& a, bool alibi, cudaStream_t stream) {
   if (a.max_splits > 0) {
-    const dim3 grid(a.max_splits, a.Hkv * a.head_blocks, a.B);
-    constexpr auto with = kv4_decode_kernel<D, BF16, true>;
-    constexpr auto without = kv4_decode_kernel<D, BF16, false>;
-    cudaError_t e = alibi ? set_smem_once<with>(KSmem<D>::kBytes)
-                          : set_smem_once<without>(KSmem<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    if (alibi) with<<<grid, kThreads, KSmem<D>::kBytes, stream>>>(a);
-    else without<<<grid, kThreads, KSmem<D>::kBytes, stream>>>(a);
-    e = cudaGetLastError();
+    const dim3 grid(a.Hkv * a.head_blocks, a.B, a.max_splits);
+    // Up to four heads at K = 128: a column for each (group, head).
+    cudaError_t e;
+    if (D == 128 && a.group <= 4)
+      e = alibi ? decode_run<D, BF16, true, D == 128>(a, grid, stream)
+                : decode_run<D, BF16, false, D == 128>(a, grid, stream);
+    else
+      e = alibi ? decode_run<D, BF16, true, false>(a, grid, stream)
+                : decode_run<D, BF16, false, false>(a, grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.part_o == nullptr && a.max_splits > 0 && a.w_out == nullptr) return cudaSuccess;
