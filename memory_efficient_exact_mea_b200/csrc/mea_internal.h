@@ -250,6 +250,7 @@ struct WeightArgs {
   int* status;
   int B, M, N, Hq, Hkv, group;
   float scale_log2;
+  int parts;                 // many rows only: CTAs (a cluster) that share a key block
   int few_chunk;             // few rows only: keys per CTA (a multiple of 64)
   long long q_s[3], k_s[3];  // few rows only: element strides (b, row, head)
 };

@@ -10,11 +10,12 @@
 // tensor memory has a key per lane, so the sum over queries is a sum along each
 // thread's own row -- no reduction across lanes, no atomics, the same order every
 // time.  For each 128 keys, two groups of four warps take alternate tiles (one TMEM
-// buffer each), so one group's exponentials overlap the other's MMA and TMEM read.  Bound by
-// the exponential unit (16 a clock per SM).
+// buffer each), so one group's exponentials overlap the other's MMA and TMEM read.
+// Bound by the exponential unit (16 a clock per SM; 75 % busy at K = 128).
 //
 // A few query rows (a decode step, a short chunk) go to weights_few_kernel: the same
 // sum with mma.sync straight from global memory, bound by reading K once.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <type_traits>
@@ -25,6 +26,9 @@
 namespace mea {
 namespace {
 
+namespace cg = cooperative_groups;
+
+constexpr int kMaxWeightParts = 8;  // CTAs of a cluster that share a key block
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -91,7 +95,8 @@ struct WCfg {
   static constexpr int kLse = kQ + kStages * kQTile;      // [slot][NQ] -lse * log2(e)
   static constexpr int kSlope = kLse + kLseSlots * NQ * 4;  // [slot] the tile's ALiBi slope
   static constexpr int kSum = kSlope + kLseSlots * 4;      // [kKeys]
-  static constexpr int kBar = kSum + kKeys * 4;
+  static constexpr int kPart = kSum + kKeys * 4;           // [kMaxWeightParts][kKeys]
+  static constexpr int kBar = kPart + kMaxWeightParts * kKeys * 4;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kLseSlots + 4 * kHalves;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
@@ -125,11 +130,12 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The key block varies slowest: under a causal mask the first blocks, seen by
-  // the most query rows, start first; CTAs of one (kv head, sequence) read the
-  // same query tiles from L2 at about the same time.
+  // the most query rows, start first.  The a.parts CTAs of a cluster share a block's
+  // (head, row block) pairs.
   const int per = a.Hkv * a.B;
-  const int nb = blockIdx.x / per;
-  const int bh = blockIdx.x - nb * per;
+  const int unit = blockIdx.x / a.parts, part = blockIdx.x - unit * a.parts;
+  const int nb = unit / per;
+  const int bh = unit - nb * per;
   const int b = bh / a.Hkv, kvh = bh - b * a.Hkv;
   const int n0 = nb * C::kKeys;
 
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
   const int past = a.cache_len ? a.cache_len[b] : a.N - a.M;
   const long long wrow = static_cast<long long>(bh) * a.N;
   if (m < 0 || m > a.M || (a.cache_len && past < 0) || past > a.N - m) {
-    if (nb == 0 && kvh == 0 && threadIdx.x == 0) record_error(a.status, kErrInvalidArg);
+    if (nb == 0 && kvh == 0 && part == 0 && threadIdx.x == 0)
+      record_error(a.status, kErrInvalidArg);
     return;
   }
   // without cache_len the N keys are all there, whatever m is
@@ -146,14 +153,17 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
   int m_first = 0;
   if constexpr (CAUSAL) m_first = max(0, n0 - past) / NQ * NQ;
   const int mblocks = m > m_first ? (m - m_first + NQ - 1) / NQ : 0;
-  const int steps = n0 < n ? a.group * mblocks : 0;
-  if (steps == 0) {  // no query sees these keys
-    if (threadIdx.x < C::kKeys && n0 + static_cast<int>(threadIdx.x) < a.N) {
+  const int total = n0 < n ? a.group * mblocks : 0;
+  if (total == 0) {  // no query sees these keys (the same for the whole cluster)
+    if (part == 0 && threadIdx.x < C::kKeys && n0 + static_cast<int>(threadIdx.x) < a.N) {
       const int j = n0 + threadIdx.x;
       a.w_out[wrow + j] = (j < n && a.w_in) ? a.w_in[wrow + j] : 0.f;
     }
     return;
   }
+
+  const int s_first = static_cast<int>(static_cast<long long>(total) * part / a.parts);
+  const int steps = static_cast<int>(static_cast<long long>(total) * (part + 1) / a.parts) - s_first;
 
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1);
@@ -180,6 +190,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (a.parts > 1) cg::this_cluster().sync();  // every CTA runs before any reaches into another
   const uint32_t tmem_base = *tmem_slot;
 
   float sum = 0.f;
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
     }
     int issued = 0;
     for (int s = 0; s < steps; ++s) {
-      const int g = s / mblocks, m0 = m_first + (s - g * mblocks) * NQ;
+      const int g = (s_first + s) / mblocks, m0 = m_first + (s_first + s - g * mblocks) * NQ;
       const int slot = s % C::kStages, ls = s % C::kLseSlots;
       const int h = kvh * a.group + g;
       float l2[NQ / 32];
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
     f2 acc = {0.f, 0.f};
     const f2 sc2 = {a.scale_log2, a.scale_log2};
     for (int s = grp % C::kParity; s < steps; s += C::kParity) {
-      const int g = s / mblocks, m0 = m_first + (s - g * mblocks) * NQ;
+      const int g = (s_first + s) / mblocks, m0 = m_first + (s_first + s - g * mblocks) * NQ;
       const int ls = s % C::kLseSlots, buf = 2 * half + (s & 1);
       // row i = m0 + row(c) sees this key iff i >= key - past
       const int first = CAUSAL ? max(0, key - past - m0) : 0;
@@ -318,9 +329,29 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
   __syncthreads();
   tc_fence_after();
   if (warp == C::kMmaWarp) tmem_dealloc(tmem_base, C::kTmemCols);
-  if (warp < C::kWarps && (warp >> 2) % C::kParity == 0) {
+  const bool sums = warp < C::kWarps && (warp >> 2) % C::kParity == 0;
+  if (a.parts > 1) {
+    // Every CTA leaves its sums in the first one's shared memory, which adds them up
+    // in order.  (All get here: each wait above is bounded.)
+    float* s_part = reinterpret_cast<float*>(smem + C::kPart);  // [part][kKeys]
+    cg::cluster_group cluster = cg::this_cluster();
+    if (sums) {
+      const int at = (warp >> 2) / C::kParity * kWeightKeys + (warp & 3) * 32 + lane;
+      sum += s_sum[at];
+      if (*abort_flag) sum = __int_as_float(0x7fc00000);
+      cluster.map_shared_rank(s_part, 0)[part * C::kKeys + at] = sum;
+    }
+    cluster.sync();
+    if (part != 0 || !sums) return;
     const int at = (warp >> 2) / C::kParity * kWeightKeys + (warp & 3) * 32 + lane, j = n0 + at;
-    if (C::kParity == 2) sum += s_sum[at];
+    sum = 0.f;
+    for (int p = 0; p < a.parts; ++p) sum += s_part[p * C::kKeys + at];
+    if (j < a.N) a.w_out[wrow + j] = j < n ? sum + (a.w_in ? a.w_in[wrow + j] : 0.f) : 0.f;
+    return;
+  }
+  if (sums) {
+    const int at = (warp >> 2) / C::kParity * kWeightKeys + (warp & 3) * 32 + lane, j = n0 + at;
+    sum += s_sum[at];
     if (*abort_flag) sum = __int_as_float(0x7fc00000);  // a wait gave up
     if (j < a.N) a.w_out[wrow + j] = j < n ? sum + (a.w_in ? a.w_in[wrow + j] : 0.f) : 0.f;
   }
@@ -485,8 +516,26 @@ cudaError_t launch_t(const WeightLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const WeightArgs& a = L.args;
   const long long blocks = static_cast<long long>((a.N + keys - 1) / keys) * a.Hkv * a.B;
-  kern<<<static_cast<unsigned>(blocks), WCfg<D>::kThreads, smem, stream>>>(L.tmQ, L.tmK, a);
-  return cudaGetLastError();
+  // Fewer key blocks than the GPU holds CTAs: clusters of up to 8 share a block's
+  // queries, as long as each has two tiles or more.
+  const long long tiles = static_cast<long long>(a.group) * ((a.M + WCfg<D>::NQ - 1) / WCfg<D>::NQ);
+  WeightArgs args = a;
+  args.parts = 1;
+  while (args.parts < kMaxWeightParts && blocks * args.parts * 2 <= 148 * WCfg<D>::kCtas &&
+         tiles >= args.parts * 4)
+    args.parts *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * args.parts));
+  cfg.blockDim = dim3(WCfg<D>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = args.parts;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = args.parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, L.tmQ, L.tmK, args);
 }
 
 template <int D, bool BF16>

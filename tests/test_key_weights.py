@@ -130,6 +130,17 @@ def test_many_steps(mea):
     check(mea, q, k, causal=False, weigh=False)
 
 
+@pytest.mark.parametrize("K,dtype,Hq,Hkv,M,N", [(128, "bf16", 16, 1, 700, 600), (64, "f16", 4, 1, 600, 300),
+                                                (128, "f16", 9, 1, 260, 900), (64, "bf16", 3, 3, 515, 515)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_key_blocks(mea, K, dtype, Hq, Hkv, M, N, causal):
+    """Too few key blocks to fill the GPU: clusters share each block's queries."""
+    q, k = randn((1, M, Hq, K), dtype, 21), randn((1, N, Hkv, K), dtype, 22)
+    a = check(mea, q, k, causal=causal, alibi=Hkv == 3)
+    b = check(mea, q, k, causal=causal, alibi=Hkv == 3)
+    assert torch.equal(a, b)
+
+
 def test_weights_add_up_to_the_rows(mea):
     """A softmax's weights sum to one: with mea_fwd's own lse the keys gather M per head."""
     q, k = randn((2, 513, 8, 64), "f16", 9).to(DEV), randn((2, 700, 2, 64), "f16", 10).to(DEV)
