@@ -3,7 +3,7 @@
 // Of a sequence's n rows a kv head keeps, when n > budget, the newest `recent`
 // and the budget - recent heaviest of the others (equal weights: the lowest row;
 // NaN: as the lightest), in their old order.  Two launches:
-//   evict_select  one block per (sequence, kv head): the weight of the last row
+//   evict_select  a block (or a cluster) per (sequence, kv head): the weight of the last row
 //                 to keep by three counting passes over 11, 11 and 10 bits of an
 //                 order-preserving integer, then the kept row numbers by counting
 //                 in row order (ballots and a scan: no atomic decides an order);
@@ -13,6 +13,7 @@
 //                 it, and one barrier between a tile's loads and its stores is
 //                 all the order there is to keep.  Into another cache, blocks
 //                 also share out the rows.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "mea_internal.h"
@@ -20,6 +21,8 @@
 
 namespace mea {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelTile = 4 * kSelThreads;
@@ -33,16 +36,25 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+// The a.parts CTAs of a cluster take a (sequence, kv head)'s rows in equal runs, add
+// up their counts in each other's shared memory and all find the same last key.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 2)
+    evict_select_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t whole[CLUSTER ? kBins : 1];  // the cluster's sum of hist
   __shared__ uint32_t warp_sum[32];
   __shared__ uint32_t s_bin, s_above;
   __shared__ uint32_t counts[128];
-  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x - b * a.Hkv;
+  __shared__ uint32_t s_rows[2];  // this CTA's rows above the last key, and equal to it
+  const int parts = CLUSTER ? a.parts : 1;
+  const int bh = blockIdx.x / parts, part = blockIdx.x - bh * parts;
+  const int b = bh / a.Hkv, kvh = bh - b * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = a.lens[b];
-  int32_t* kept = a.kept + static_cast<long long>(blockIdx.x) * a.budget;
+  int32_t* kept = a.kept + static_cast<long long>(bh) * a.budget;
   if (n < 0 || n > a.cap) {
+    if (part != 0) return;
     if (kvh == 0 && tid == 0) {
       record_error(a.status, kErrInvalidArg);
       a.new_lens[b] = 0;
@@ -50,16 +62,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int r = tid; r < a.budget; r += kSelThreads) kept[r] = -1;
     return;
   }
-  if (kvh == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
+  if (kvh == 0 && part == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
   if (n <= a.budget) {
-    for (int r = tid; r < a.budget; r += kSelThreads) kept[r] = r < n ? r : -1;
+    for (int r = part * kSelThreads + tid; r < a.budget; r += parts * kSelThreads)
+      kept[r] = r < n ? r : -1;
     return;
   }
-  const float* w = a.weights + static_cast<long long>(blockIdx.x) * a.cap;
-  const int m = n - a.recent;        // candidates
-  const int take = a.budget - a.recent;  // < m
-  for (int r = tid; r < a.recent; r += kSelThreads) kept[take + r] = m + r;
+  const int rows = n - a.recent;         // candidates
+  const int take = a.budget - a.recent;  // < rows
+  for (int r = part * kSelThreads + tid; r < a.recent; r += parts * kSelThreads)
+    kept[take + r] = rows + r;
   if (take == 0) return;
+  // this CTA's rows [lo, lo + m); every exit above is the whole cluster's
+  const int per = (rows + parts - 1) / parts;
+  const int lo = min(rows, part * per), m = min(rows, lo + per) - lo;
+  const float* w = a.weights + static_cast<long long>(bh) * a.cap + lo;
+  [[maybe_unused]] cg::cluster_group cluster = cg::this_cluster();
 
   const bool held = m <= kSelHeld * kSelThreads;
   uint32_t mine[kSelHeld];
@@ -97,8 +115,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
     }
     __syncthreads();
+    if constexpr (CLUSTER) {
+      cluster.sync();  // all have counted
+      for (int i = tid; i < kBins; i += kSelThreads) {
+        uint32_t sum = 0;
+        for (int r = 0; r < parts; ++r) sum += cluster.map_shared_rank(hist, r)[i];
+        whole[i] = sum;
+      }
+      cluster.sync();  // all have read: hist may be cleared
+    }
+    const uint32_t* bins = CLUSTER ? whole : hist;
     // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-    const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+    const uint32_t c0 = bins[kBins - 1 - 2 * tid], c1 = bins[kBins - 2 - 2 * tid];
     uint32_t sum = c0 + c1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -126,6 +154,34 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 
   // Rows above the key `prefix` are kept, and the first `need` equal to it.
   uint32_t base = 0, base_eq = 0;  // rows before this tile: above, and equal
+  if constexpr (CLUSTER) {
+    if (tid < 2) s_rows[tid] = 0;
+    __syncthreads();
+    uint32_t above = 0, equal = 0;
+    auto tally = [&](uint32_t key) {
+      above += key > prefix;
+      equal += key == prefix;
+    };
+    if (held) {
+#pragma unroll
+      for (int u = 0; u < kSelHeld; ++u)
+        if (u * kSelThreads + tid < m) tally(mine[u]);
+    } else {
+      for (int j = tid; j < m; j += kSelThreads) tally(order_key(w[j]));
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {  // whole numbers: the order of the additions does not matter
+      atomicAdd(&s_rows[0], above);
+      atomicAdd(&s_rows[1], equal);
+    }
+    cluster.sync();
+    for (int r = 0; r < part; ++r) {
+      base += cluster.map_shared_rank(s_rows, r)[0];
+      base_eq += cluster.map_shared_rank(s_rows, r)[1];
+    }
+    cluster.sync();  // no CTA ends while another reads its counts
+  }
   auto place = [&](int t0, const uint32_t(&keys)[4]) {
     uint32_t gt[4], eq[4];
 #pragma unroll
@@ -163,7 +219,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       const uint32_t neq = base_eq + (c >> 16) + __popc(eq[u] & lower);
       const bool is_eq = (eq[u] >> lane) & 1u;
       if (((gt[u] >> lane) & 1u) || (is_eq && neq < need))
-        kept[ngt + min(neq, need)] = t0 + u * kSelThreads + tid;
+        kept[ngt + min(neq, need)] = lo + t0 + u * kSelThreads + tid;
     }
     base += warp_sum[0] & 0xffffu;
     base_eq += warp_sum[0] >> 16;
@@ -308,8 +364,25 @@ __global__ void __launch_bounds__(kMoveThreads)
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  evict_select_kernel<<<a.B * a.Hkv, kSelThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // Long caches of few (sequence, head)s: clusters share the rows, down to the number
+  // a CTA holds (131072 rows of 8 heads took one CTA each 117 us).
+  EvictArgs args = a;
+  args.parts = 1;
+  while (args.parts < 8 && a.cap > args.parts * kSelHeld * kSelThreads &&
+         a.B * a.Hkv * args.parts * 2 <= 148 * 2)
+    args.parts *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.B * a.Hkv * args.parts);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = args.parts;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = args.parts > 1 ? 1 : 0;
+  const cudaError_t e = args.parts > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, args)
+                                       : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, args);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.first_block[a.n_planes], a.B * a.Hkv,
                   (a.budget + a.seg_rows - 1) / a.seg_rows);

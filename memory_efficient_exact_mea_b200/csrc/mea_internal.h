@@ -286,6 +286,7 @@ struct EvictArgs {
   int n_planes;
   int seg_rows;              // kept rows one move block takes (budget when anything is in place)
   bool in_place;             // some plane or the weights
+  int parts;                 // CTAs (a cluster) that choose for one (sequence, kv head)
   const float* weights;      // [B, Hkv, cap]
   float* w_out;              // [B, Hkv, out_rows]
   const int32_t* lens;       // [B]

@@ -140,6 +140,14 @@ def test_long(mea, in_place, kind):
     run(mea, False, kind, [9001, 5000], 4100, 100, K=64, Hkv=1, cap=9007, in_place=in_place)
 
 
+@pytest.mark.parametrize("cap,lens,Hkv", [(20000, [20000, 9], 1), (70001, [70000], 2),
+                                          (140000, [131072], 1), (140000, [140000, 30000], 1)])
+@pytest.mark.parametrize("kind", ["random", "ties", "odd"])
+def test_clusters(mea, cap, lens, Hkv, kind):
+    """Long caches of few heads: the rows of one choice shared by 2 to 8 CTAs."""
+    run(mea, True, kind, lens, 3000, 17, K=64, Hkv=Hkv, cap=cap, out_rows=3001)
+
+
 def test_many_heads(mea):
     run(mea, True, "wide", [150] * 40, 33, 5, K=64, Hkv=16, cap=151)
 
