@@ -52,6 +52,7 @@ DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
   const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
   int64_t chunk = (max_len + want - 1) / want;
   chunk = std::min<int64_t>(1536, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  chunk = std::max<int64_t>(chunk, ((max_len + int64_t(65534)) / 65535 + 127) / 128 * 128);
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);
   return p;
@@ -368,6 +369,10 @@ int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weight
       // planes of one cache may interleave (a key and a value view of one array)
       const bool same_array = all[d].src == all[d].dst && all[s].src == all[s].dst;
       if (!same_array && d0 < s1 && s0 < d1) return MEA_ERR_INVALID_ARG;
+      // two planes written to the same rows
+      const uint8_t* e0 = a.planes[s].dst;
+      const int64_t apart = d0 < e0 ? e0 - d0 : d0 - e0;
+      if (d < s && apart < (d0 < e0 ? all[d] : all[s]).row_bytes) return MEA_ERR_INVALID_ARG;
     }
 
   // Blocks: (column piece of a plane) x (sequence, kv head) x row segment.  Into

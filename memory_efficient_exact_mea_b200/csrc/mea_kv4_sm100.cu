@@ -739,8 +739,9 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       }
     };
     weigh();
-    if (__any_sync(0xffffffffu, heavy[0] > kMaxWeight || heavy[1] > kMaxWeight ||
-                                    sum[0] > kMaxPlain || sum[1] > kMaxPlain)) {
+    // (a NaN among the sums hides the others, so it counts as an overflow)
+    if (__any_sync(0xffffffffu, !(heavy[0] <= kMaxWeight && heavy[1] <= kMaxWeight &&
+                                  sum[0] <= kMaxPlain && sum[1] <= kMaxPlain))) {
       // Raise the reference: the largest p s of these rows becomes about one, and p
       // of that row a power of two (a lone row's lse is then exact).  A row whose
       // step is small beside its zero counts with 2^-12 of the zero, so that p z

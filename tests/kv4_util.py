@@ -4,9 +4,11 @@ one (sequence, head) at a time, and the error bounds their tests use.
 Bounds (u32 = 2^-24 a rounding of fp32, 2^-23 a truncating tensor-core addition;
 h16 = half a step of the 16-bit type, 2^-8 bf16 or 2^-11 fp16, relative):
   score  a dot product of K terms summed in fp32 is off by at most K 2^-23 times
-         the sum of its terms' magnitudes.  The 4-bit decode sums q (16 + c) and
-         takes 16 sum q off again: magnitudes |q| (s (16 + c) + |z - 16 s|).
-  weight exp of a score off by e is off by a factor e^e; exp2 itself by 2^-22.
+         the sum of its terms' magnitudes.  The 4-bit decode sums s q c and z q apart:
+         magnitudes |q| (15 s + |z|).
+  weight exp of a score off by e is off by a factor e^e; exp2 itself by 2^-22.  The
+         4-bit decode multiplies p s held as one fp16 number (half a step 2^-11) for
+         bf16 results and as two (2^-21) for fp16 results.
   sum    n terms added in fp32: n 2^-24 of the sum of magnitudes.
 """
 from __future__ import annotations
@@ -16,6 +18,7 @@ import math
 import torch
 
 HALF = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+HELD = {torch.float16: 2.0 ** -21, torch.bfloat16: 2.0 ** -11}  # of p s
 
 
 def quantise(x):
@@ -74,10 +77,10 @@ def decode(q, cache, lens, scale, alibi=False):
         for j in range(Hkv if n else 0):
             k, v = values(kc[b, j, :n], kp[b, j, :n]), values(vc[b, j, :n], vp[b, j, :n])
             s, z = kp[b, j, :n, :, 0].double(), kp[b, j, :n, :, 1].double()
-            mag = (31 * s.abs() + (z - 16 * s).abs()).repeat_interleave(64, -1)  # [n, K]
+            mag = (15 * s.abs() + z.abs()).repeat_interleave(64, -1)  # [n, K]
             vs = vp[b, j, :n, :, 0].double().abs()
             vz = vp[b, j, :n, :, 1].double().abs()
-            vmag = (31 * vs + 16 * vs + vz).amax(0).repeat_interleave(64)  # [K]
+            vmag = (15 * vs + vz).amax(0).repeat_interleave(64)  # [K]
             for g in range(G):
                 h = j * G + g
                 qd = q[b, h].double()
@@ -93,9 +96,9 @@ def decode(q, cache, lens, scale, alibi=False):
                 lse[b, h], out[b, h] = L, p @ v
                 w[b, j, :n] += p
                 e_lse[b, h] = e + n * 2.0 ** -24
-                # weights off by a factor 1 + 2e, p s held in 16 bits or more, n + 2K sums
-                rel = 2 * (math.expm1(e) + n * 2.0 ** -23 + 2.0 ** -16)
-                e_out[b, h] = vmag * rel + out[b, h].abs() * HALF[q.dtype]
+                # a weight and their sum off by a factor e^e each, n sums, the held p s
+                rel = 2 * (math.expm1(e) + n * 2.0 ** -23)
+                e_out[b, h] = vmag * (rel + HELD[q.dtype]) + out[b, h].abs() * HALF[q.dtype]
                 e_w[b, j, :n] += p * rel
     return (out, lse, w), (e_out, e_lse, e_w)
 

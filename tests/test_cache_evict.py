@@ -179,6 +179,17 @@ def test_strided_and_interleaved_caches(mea):
             assert torch.equal(both[b, h, budget:], before[b, h, budget:])
 
 
+def test_one_array_as_keys_and_values_is_refused(mea):
+    x = torch.zeros(1, 20, 1, 64, device=DEV).half()
+    w = torch.zeros(1, 1, 20, device=DEV)
+    with pytest.raises(mea.MeaError):
+        mea.mea_cache_evict((x, x), w, i32([20]), 5, 1)
+    # read from one array into two it is a copy like any other
+    out = (torch.empty_like(x), torch.empty_like(x))
+    new, kept, _ = mea.mea_cache_evict((x, x), w, i32([20]), 5, 1, out=out)
+    assert kept.tolist() == [[[0, 1, 2, 3, 19]]] and new.tolist() == [5]
+
+
 def test_bad_lengths_are_reported(mea):
     src = [t.to(DEV) for t in make(False, 2, 50, 2, 64, 1)]
     w = weights("random", 2, 2, 50, 2).to(DEV)

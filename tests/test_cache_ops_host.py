@@ -111,6 +111,8 @@ def evict(plane=None, n=1, w=P(1 << 20), wo=P(2 << 20), lens=P(16), new=P(64), k
     (dict(dst=(1 << 24) + 320), INVALID),              # overlaps its source
     (dict(dst=1 << 20), INVALID),                      # overlaps the weights
     (dict(wo=P(1 << 20)), INVALID),                    # weights in place, but fewer rows
+    (dict(n=2, dst=(1 << 25) + 1024), INVALID),        # two planes into the same rows
+    (dict(n=2, dst=(1 << 25) + 1032), INVALID),
     (dict(B=0), OK)])
 def test_evict(kw, code):
     assert evict(**kw) == code

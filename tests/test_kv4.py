@@ -305,6 +305,27 @@ def test_decode_nan_stays_in_its_head(mea):
     assert torch.isfinite(w[0, 0]).all() and torch.isfinite(w[1]).all()
 
 
+@pytest.mark.parametrize("Hq", [4, 6])
+def test_decode_nan_value_stays_in_its_group(mea, Hq):
+    """A NaN among one group of V's dimensions leaves the other group's results alone, also
+    while the maximum is moving."""
+    n, K = 300, 128
+    q = torch.randn(1, Hq, K, generator=gen(51)).bfloat16()
+    k = (q[:, None, :1].float() * torch.linspace(-3, 6, n).view(1, n, 1, 1)).bfloat16()
+    v = rows((1, n, 1, K), "bf16", 52)
+    clean = mea.mea_kv4_alloc(1, n, 1, K, torch.bfloat16, DEV)
+    mea.mea_kv4_append(k.to(DEV), v.to(DEV), clean, i32([0]))
+    want, lse = mea.mea_decode_kv4(q.to(DEV), clean, i32([n]), n)
+    _, (eo, el, _) = U.decode(q, [t.cpu() for t in clean], [n], K ** -0.5)
+    v[0, ::7, 0, 3] = math.nan
+    mea.mea_kv4_append(k.to(DEV), v.to(DEV), clean, i32([0]))
+    got, lse2 = mea.mea_decode_kv4(q.to(DEV), clean, i32([n]), n)
+    assert torch.isnan(got[..., :64]).all() and torch.isfinite(got[..., 64:]).all()
+    # the reference may move at other rows: each side lies within its bound of the value
+    assert ((got - want).double().cpu().abs() <= 2 * eo)[..., 64:].all()
+    assert ((lse - lse2).double().cpu().abs() <= 2 * el).all()
+
+
 def test_decode_bad_lengths_are_reported(mea):
     lens = [10, 10, 10]
     cache = make_cache(mea, lens, 20, 2, 64, "f16", spoil=False)
