@@ -34,13 +34,18 @@ bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
 }
 
 // mea_key_weights with at most this many query rows and (row, query head) pairs a kv
-// head goes to the kernel that reads K once with mma.sync.
-constexpr int kFewRows = 16, kFewColumns = 128;
+// head goes to the kernel that reads K once with mma.sync.  8 x 8 heads x 8192 keys,
+// K = 128, us here / with 128-row tiles: one row 37 / 90 (one query head), 37 / 158
+// (four), 36 / 250 (eight); 64 pairs 57 / 90, 57 / 157, 55 / 249; 128 pairs 88 / 158
+// (32 rows x 4), 86 / 249.  Full tiles win once they are full.
+constexpr int kFewRows = 64, kFewColumns = 128;
 
 // Splits of one decode call.  A split is a whole number of 128-row steps (four
 // warps of 32 rows); long enough that its partial state (K floats a head) and
 // its start-up stay small beside the rows it reads, short enough that the grid
-// fills the GPU's resident CTAs a few times over.
+// fills the GPU's resident CTAs a few times over: at most 768 / 1024 / 1536 / 2048
+// rows took 82.7 / 79.5 / 78.1 / 79.6 us for 64 sequences of up to 8192 rows and
+// 67.0 / 64.0 / 63.1 / 64.6 us for four of up to 65521.
 struct DecodePlan {
   int head_blocks, chunk, splits;
 };

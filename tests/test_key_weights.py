@@ -95,7 +95,7 @@ def test_forward_shapes(mea, K, dtype, M, N, causal):
 
 @pytest.mark.parametrize("K,dtype", [(64, "f16"), (128, "bf16")])
 @pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2), (5, 1), (21, 1), (32, 2)])
-@pytest.mark.parametrize("M", [1, 2, 7, 16])
+@pytest.mark.parametrize("M", [1, 2, 7, 16, 33, 64, 65])
 def test_few_rows(mea, K, dtype, Hq, Hkv, M):
     """Decode steps and short chunks: the heads of a group share a tile."""
     past, new = [0, 5, 250, 128], [M, M - 1, M, M]
