@@ -331,10 +331,14 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // a largest magnitude below 256, exact but for values 2^-22 of that and less.
 // P' = p s goes in as one fp16 number for bf16 results (11 bits against the result's
 // 8: the error against 64 bits stays at the result's own rounding) and as two, high
-// and low, for fp16 results (one would double their error).  The reference R of
-// p = 2^(y - R) is chosen per head so that the largest p s is about one, not the
-// largest p, and is raised only when some p s passes 2^14 (so the accumulators are
-// rarely rescaled).
+// and low, for fp16 results (one would double their error).  p = 2^(y - ref) with ref
+// the running maximum of a head's scores; what goes in is p s F, F a power of two for
+// each (head, group of 64 dimensions) that puts the largest p s so far at 2^4, so that
+// a group keeps its bits however small its steps are beside the other group's.  fp16's
+// range then ends 28 powers of two below a group's largest p s; a row that far below
+// adds less than the sum's own rounding.  ref and F move only when some p s F passes
+// 2^15 or some p 2^11 (so the accumulators are rarely rescaled), or when p z F, kept in
+// fp32, passes 2^100.
 //
 // A warp takes 32 rows at a time in the fragment layout of mma.sync m16n8k16 (rows
 // x heads and dimensions x heads, heads padded to 8): a thread's nibbles for one
@@ -354,8 +358,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;        // rows per warp and iteration
 constexpr int kHeads = 8;        // query heads per CTA (MMA n)
 constexpr float kNoRef = -3.0e38f;     // reference of a warp that has seen no score
-constexpr float kMaxWeight = 16384.f;  // largest p s before the reference is raised
-constexpr float kMaxPlain = 0x1p64f;   // the same for p alone (rows whose s is small)
+constexpr float kMaxWeight = 32768.f;  // largest p s F before ref and F are set anew
+constexpr float kTarget = 4.f;         // log2 of the largest p s F then
+constexpr float kPerPlain = 16.f;      // a p of 2^11 counts as much as a p s F of 2^15,
+constexpr float kPerZero = 0x1p-85f;   // and a p z F of 2^100
+// F <= 2^112, so that p F stays in fp32's range: groups whose steps are all below
+// 2^-108 reach fp16's subnormals earlier.
+constexpr float kLeastFactor = -126.f, kMostFactor = 112.f;  // log2
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
@@ -387,6 +396,14 @@ __device__ __forceinline__ CodePairs code_pairs(uint32_t w) {
 }
 constexpr float kUnitEven = 0x1p24f, kUnitOdd = 0x1p20f;  // what brings them back to c
 
+// log2 of a normal power of two, and back.
+__device__ __forceinline__ float log2_of(float f) {
+  return static_cast<float>((__float_as_int(f) >> 23) - 127);
+}
+__device__ __forceinline__ float power_of_two(float e) {
+  return __int_as_float((static_cast<int>(e) + 127) << 23);
+}
+
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if constexpr (BYTES == 16)
@@ -417,8 +434,9 @@ struct KSmem {
   static constexpr int kStage = 2 * (kCodes + kParams);  // K codes, V codes, K params, V params
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kBytes = kWarps * kWarp;
-  // after the ring: m, l [kWarps][kHeads], acc [kWarps][kHeads][D]
-  static_assert(kWarps * kHeads * (D + 2) * 4 <= kBytes, "combine area");
+  // after the ring: ref, l [kWarps][kHeads], log2 of acc's unit [kWarps][kHeads][NG],
+  // acc [kWarps][kHeads][D]
+  static_assert(kWarps * kHeads * (D + 2 + NG) * 4 <= kBytes, "combine area");
 };
 
 // Where 16-byte chunk c of row r of a tile lies: 128-byte lines, the chunk's slot
@@ -597,9 +615,12 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
   }
 
   float ref[2] = {kNoRef, kNoRef}, l_part[2] = {0.f, 0.f};
-  float zacc[NT][2], acc[D / 16][4];
+  float fac[NT][2], zacc[NT][2], acc[D / 16][4];
 #pragma unroll
-  for (int g = 0; g < NT; ++g) zacc[g][0] = zacc[g][1] = 0.f;
+  for (int g = 0; g < NT; ++g) {
+    fac[g][0] = fac[g][1] = 1.f;
+    zacc[g][0] = zacc[g][1] = 0.f;
+  }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -699,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
             if (t + 8 * i + gid < s1) out[8 * i] = y[i >> 1][2 * (i & 1) + e] * unit[e];
         }
     }
-    // Weights of the tile against the present reference: p s in fp16, and the sums
-    // of p, p s and p z (an overflow shows in a sum of numbers >= 0).
+    // Weights of the tile against the present reference: p s F in fp16, and the sums
+    // of p, p s F and p z F (an overflow shows in a sum of numbers >= 0).
     constexpr int kParts = BF16 ? 1 : 2;
     uint32_t pk[2][NT][2][kParts];
     float sum[2], heavy[2], zsum[NT][2];
@@ -724,11 +745,12 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
           const float s = step_of<BF16>(vq[i][g]), z = zero_of<BF16>(vq[i][g]);
-          const float ps0 = p[0] * s, ps1 = p[1] * s;
+          const float pf0 = p[0] * fac[g][0], pf1 = p[1] * fac[g][1];
+          const float ps0 = pf0 * s, ps1 = pf1 * s;
           heavy[0] += ps0;
           heavy[1] += ps1;
-          zsum[g][0] = fmaf(p[0], z, zsum[g][0]);
-          zsum[g][1] = fmaf(p[1], z, zsum[g][1]);
+          zsum[g][0] = fmaf(pf0, z, zsum[g][0]);
+          zsum[g][1] = fmaf(pf1, z, zsum[g][1]);
           uint32_t(&out)[kParts] = pk[i >> 1][g][i & 1];
           out[0] = pack2<false>(ps0, ps1);
           if constexpr (kParts == 2)
@@ -739,40 +761,51 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       }
     };
     weigh();
-    // (a NaN among the sums hides the others, so it counts as an overflow)
-    if (__any_sync(0xffffffffu, !(heavy[0] <= kMaxWeight && heavy[1] <= kMaxWeight &&
-                                  sum[0] <= kMaxPlain && sum[1] <= kMaxPlain))) {
-      // Raise the reference: the largest p s of these rows becomes about one, and p
-      // of that row a power of two (a lone row's lse is then exact).  A row whose
-      // step is small beside its zero counts with 2^-12 of the zero, so that p z
-      // stays in range too.
+    // One sum tells of them all (a NaN hides the others, so it counts as an overflow).
+    float over = heavy[0] + heavy[1] + kPerPlain * (sum[0] + sum[1]);
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+      over = fmaf(kPerZero, fabsf(zsum[g][0]) + fabsf(zsum[g][1]), over);
+    if (__any_sync(0xffffffffu, !(over <= kMaxWeight))) {
+      // Set ref and F anew.  A row whose step is small beside its zero counts with
+      // 2^-12 of the zero, so that p z F stays in range too.
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        auto over_rows = [](float v) {  // the warp's rows of a column
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        };
         float v = neg_inf();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float mag = 0x1p-60f;
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, y[i >> 1][2 * (i & 1) + e] * unit[e]);
+        const float r_new = fmaxf(ref[e], over_rows(v));
+        const float drop = r_new == ref[e] ? 0.f : ref[e] - r_new;
+        l_part[e] *= ex2(drop);
 #pragma unroll
-          for (int g = 0; g < NT; ++g)
-            mag = fmaxf(mag, fmaxf(step_of<BF16>(vq[i][g]),
-                                   fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f));
-          v = fmaxf(v, y[i >> 1][2 * (i & 1) + e] * unit[e] + rintf(__log2f(mag)));
+        for (int g = 0; g < NT; ++g) {
+          float m = neg_inf();  // log2 of the largest p s, against a reference of zero
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mag = fmaxf(step_of<BF16>(vq[i][g]),
+                                    fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f);
+            m = fmaxf(m, y[i >> 1][2 * (i & 1) + e] * unit[e] + __log2f(mag));
+          }
+          const float f_old = log2_of(fac[g][e]);
+          m = fmaxf(over_rows(m), ref[e] + (kTarget - f_old));
+          const float f_new =
+              fminf(fmaxf(rintf(kTarget + (r_new - m)), kLeastFactor), kMostFactor);
+          fac[g][e] = power_of_two(f_new);
+          const float alpha = ex2(drop + (f_new - f_old));
+          zacc[g][e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            if (PAIR || (i >> 2) == g) {
+              acc[i][e] *= alpha;
+              acc[i][e + 2] *= alpha;
+            }
         }
-        if constexpr (PAIR) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float r_new = fmaxf(ref[e], v);
-        const float alpha = r_new == ref[e] ? 1.f : ex2(ref[e] - r_new);
         ref[e] = r_new;
-        l_part[e] *= alpha;
-#pragma unroll
-        for (int g = 0; g < NT; ++g) zacc[g][e] *= alpha;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          acc[i][e] *= alpha;
-          acc[i][e + 2] *= alpha;
-        }
       }
       weigh();
     }
@@ -831,12 +864,18 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
   __syncthreads();  // the rings are read: their memory joins the warps' states
   float* c_ref = reinterpret_cast<float*>(smem);
   float* c_l = c_ref + kWarps * kHeads;
-  float* c_acc = c_l + kWarps * kHeads;
-  if (gid == 0 && own == 0) {
+  float* c_unit = c_l + kWarps * kHeads;
+  float* c_acc = c_unit + kWarps * kHeads * NG;
+  if (gid == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      c_ref[warp * kHeads + hp + e] = ref[e];
-      c_l[warp * kHeads + hp + e] = l_part[e];
+      const int at = warp * kHeads + hp + e;
+      if (own == 0) {
+        c_ref[at] = ref[e];
+        c_l[at] = l_part[e];
+      }
+#pragma unroll
+      for (int g = 0; g < NT; ++g) c_unit[at * NG + own + g] = ref[e] - log2_of(fac[g][e]);
     }
   }
 #pragma unroll
@@ -851,18 +890,22 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
     const int g = idx / D, d = idx - g * D;
-    float mx = kNoRef;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, c_ref[w * kHeads + g]);
-    float lsum = 0.f, o = 0.f;
+    const float* units = c_unit + g * NG + d / 64;  // of warp w: units[w * kHeads * NG]
+    float mx = kNoRef, top = neg_inf();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float wgt = ex2(c_ref[w * kHeads + g] - mx);  // 1 if no warp has a reference
-      lsum = fmaf(wgt, c_l[w * kHeads + g], lsum);
-      o = fmaf(wgt, c_acc[(w * kHeads + g) * D + d], o);
+      mx = fmaxf(mx, c_ref[w * kHeads + g]);
+      top = fmaxf(top, units[w * kHeads * NG]);
+    }
+    float lsum = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {  // factors of 1 if no warp has a reference
+      lsum = fmaf(ex2(c_ref[w * kHeads + g] - mx), c_l[w * kHeads + g], lsum);
+      o = fmaf(ex2(units[w * kHeads * NG] - top), c_acc[(w * kHeads + g) * D + d], o);
     }
     const long long row = static_cast<long long>(b) * a.Hq + h0 + g;
-    const float val = lsum == 0.f ? 0.f : o / lsum;  // a NaN stays a NaN
+    // a NaN stays a NaN; the units' difference lies in -kMostFactor .. -kLeastFactor
+    const float val = lsum == 0.f ? 0.f : o / lsum * ex2(top - mx);
     const float lse2 = lsum == 0.f ? neg_inf() : mx + log2f(lsum);
     if (a.part_o == nullptr) {  // the only split
       static_cast<uint16_t*>(a.out)[row * D + d] = static_cast<uint16_t>(to_16<BF16>(val));

@@ -1,0 +1,166 @@
+"""The 4-bit decode over its whole range of values: groups of very different size, values
+near the ends of the type, and every row's place in the result (bounds in kv4_bounds)."""
+import math
+
+import pytest
+import torch
+
+from kv4_bounds import decode_bound
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def mea():
+    import memory_efficient_exact_mea_b200 as m
+
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status(mea):
+    mea.read_device_status()
+    yield
+    torch.cuda.synchronize()
+    assert mea.read_device_status() == 0
+
+
+def randn(shape, seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def filled(mea, k, v, lens):
+    """A 4-bit cache that holds rows k, v [B, n, Hkv, K]."""
+    B, n, Hkv, K = k.shape
+    cache = mea.mea_kv4_alloc(B, n, Hkv, K, k.dtype, DEV)
+    mea.mea_kv4_append(k.to(DEV), v.to(DEV), cache, i32([0] * B), i32(lens))
+    return cache
+
+
+def check(mea, q, k, v, lens, scale, alibi=False):
+    cache = filled(mea, k, v, lens)
+    out, lse = mea.mea_decode_kv4(q.to(DEV), cache, i32(lens), max(lens), scale=scale, alibi=alibi)
+    (ro, rl), (eo, el) = decode_bound(q, [t.cpu() for t in cache], lens, scale, alibi)
+    err = (out.double().cpu() - ro).abs()
+    assert torch.isfinite(out).all()
+    assert (err <= eo).all(), float((err / eo).max())
+    fin = ~torch.isneginf(rl)
+    assert torch.equal(torch.isneginf(lse.cpu()), ~fin)
+    assert ((lse.double().cpu() - rl).abs()[fin] <= el[fin]).all()
+    return out, cache
+
+
+SIZES = [("bf16", 1.0, 1e-3), ("bf16", 1e-5, 1.0), ("bf16", 1.0, 1e-6), ("bf16", 1.0, 1e-8),
+         ("bf16", 1e30, 1e-30), ("bf16", 1e-23, 1e-23), ("bf16", 1e-25, 1e-25), ("bf16", 1e-32, 1.0),
+         ("bf16", 1e37, 1e37), ("f16", 1e4, 1e-3), ("f16", 1e-3, 1e4), ("f16", 1e-4, 1e-4),
+         ("f16", 1e4, 1e4)]
+
+
+@pytest.mark.parametrize("dtype,a,b", SIZES)
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (6, 2), (6, 1), (9, 1)])
+@pytest.mark.parametrize("even", [True, False])
+def test_groups_of_any_size(mea, dtype, a, b, Hq, Hkv, even):
+    """Each group of 64 dimensions keeps its bits, whatever the other's size.  Equal weights
+    (scale 0) leave the values alone to be seen."""
+    n, K = 300, 128
+    v = randn((2, n, Hkv, K), 1) * torch.tensor([a, b]).repeat_interleave(64)
+    k, q = randn((2, n, Hkv, K), 2).to(DT[dtype]), randn((2, Hq, K), 3).to(DT[dtype])
+    check(mea, q, k, v.to(DT[dtype]), [n, 37], 0.0 if even else K ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,K", [("bf16", 64), ("bf16", 128), ("f16", 128)])
+def test_rows_of_any_size(mea, dtype, K):
+    """Rows whose sizes climb and fall by powers of two, against scores that do the reverse:
+    the reference of the scores and the factor of the values move apart."""
+    n = 900
+    size = torch.exp2(12 * torch.sin(torch.arange(n) / 70.0)).view(1, n, 1, 1)
+    v = (randn((1, n, 1, K), 4) * size).to(DT[dtype])
+    q = randn((1, 3, K), 5)
+    k = q[:, None, :1] * (-torch.log2(size) * 0.6) / q[0, 0].square().sum() * K ** 0.5
+    k = (k + 0.05 * randn((1, n, 1, K), 6)).to(DT[dtype])
+    check(mea, q.to(DT[dtype]), k, v, [n], K ** -0.5)
+    check(mea, q.to(DT[dtype]), k, v, [n], K ** -0.5, alibi=True)
+
+
+@pytest.mark.parametrize("K,Hq", [(64, 2), (128, 2), (128, 6)])
+@pytest.mark.parametrize("z", [1e21, -3e38, 1e-30])
+def test_equal_values_after_zeros(mea, K, Hq, z):
+    """Rows of zeros (step and zero both 0), then rows of one large value each."""
+    n = 300
+    v = torch.zeros(1, n, 1, K)
+    v[:, 140:] = z
+    k, q = 0.1 * randn((1, n, 1, K), 7), randn((1, Hq, K), 8)
+    check(mea, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n], K ** -0.5)
+
+
+PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
+          4498, 4499]
+
+
+@pytest.mark.parametrize("K,dtype,Hq,copies", [(128, "bf16", 4, 1), (128, "f16", 6, 1),
+                                               (64, "f16", 2, 1), (64, "bf16", 2, 30)])
+def test_one_row_at_a_time(mea, K, dtype, Hq, copies):
+    """A key that takes all the weight at each of many rows (copies: enough sequences for the
+    longest splits): the result is that row's values, the others' weight below e^-40."""
+    n, B = 4500, len(PROBES) * copies
+    k, v = 0.1 * randn((1, n, 1, K), 9), randn((1, n, 1, K), 10)
+    q = randn((1, Hq, K), 11).sign() + 0.25 * randn((1, Hq, K), 12)
+    base = filled(mea, k.to(DT[dtype]), v.to(DT[dtype]), [n])
+    cache = mea.Kv4Cache(*(t.repeat(B, *[1] * (t.dim() - 1)).contiguous() for t in base))
+    key = q[:, None, :1] * 8  # scores 8 |q|^2 / sqrt(K) >= 60 for head 0
+    rows = (PROBES * copies)[:B]
+    for t in (0, 1):
+        spot = filled(mea, key.to(DT[dtype]), key.to(DT[dtype]), [1])[t]
+        for b, r in enumerate(rows):
+            cache[t][b, :, r] = spot[0, :, 0]
+    qd = q.to(DT[dtype]).repeat(B, 1, 1)
+    out, lse = mea.mea_decode_kv4(qd.to(DEV), cache, i32([n] * B), n)
+    few = mea.Kv4Cache(*(t[:len(PROBES)] for t in cache))
+    (ro, rl), (eo, el) = decode_bound(qd[:len(PROBES), :1].contiguous(), [t.cpu() for t in few],
+                                      [n] * len(PROBES), K ** -0.5)
+    k16, v16 = mea.mea_kv4_read(base, i32([n]))
+    for i, r in enumerate(PROBES):  # the oracle itself says that this row is the answer
+        assert ((ro[i, 0] - v16[0, r, 0].double().cpu()).abs() <= 2.0 ** -7 * 8).all()
+    for c in range(copies):
+        at = slice(c * len(PROBES), (c + 1) * len(PROBES))
+        assert ((out[at, :1].double().cpu() - ro).abs() <= eo).all()
+        assert ((lse[at, :1].double().cpu() - rl).abs() <= el).all()
+
+
+@pytest.mark.parametrize("K,dtype,Hq,B", [(128, "bf16", 4, 2), (128, "f16", 8, 2), (64, "bf16", 3, 2),
+                                          (64, "f16", 4, 160)])
+@pytest.mark.parametrize("n", [4500, 4481, 1536, 129, 33])
+def test_every_row_counts_once(mea, K, dtype, Hq, B, n):
+    """Equal weights, values that are zero but in a few rows -- the last one, the last tile,
+    the edges of tiles, warps and splits: each such row adds 1/n of its values."""
+    v = torch.zeros(1, n, 1, K)
+    rows = sorted({r for r in (0, 31, 32, 127, 128, 1535, 1536, n - 32, n - 2, n - 1) if r < n})
+    v[0, rows, 0] = randn((len(rows), K), 13)
+    k, q = randn((1, n, 1, K), 14).to(DT[dtype]), randn((1, Hq, K), 15).to(DT[dtype])
+    base = filled(mea, k, v.to(DT[dtype]), [n])
+    cache = mea.Kv4Cache(*(t.repeat(B, *[1] * (t.dim() - 1)).contiguous() for t in base))
+    out, _ = mea.mea_decode_kv4(q.repeat(B, 1, 1).to(DEV), cache, i32([n] * B), n, scale=0.0)
+    (ro, _), (eo, _) = decode_bound(q, [t.cpu() for t in base], [n], 0.0)
+    assert ((out.double().cpu() - ro).abs() <= eo).all()
+    assert (ro.abs() > 8 * eo).double().mean() > 0.5  # a lost row would show
+
+
+@pytest.mark.parametrize("K,dtype,Hq,Hkv,lens", [
+    (128, "bf16", 8, 2, [4500, 1, 1023]), (128, "f16", 8, 1, [3000, 77]), (64, "f16", 6, 2, [2500]),
+    (64, "bf16", 20, 1, [700])])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_close_bound(mea, K, dtype, Hq, Hkv, lens, alibi):
+    """Ordinary inputs within the closer bound."""
+    n, B = max(lens), len(lens)
+    k, v = randn((B, n, Hkv, K), 16), randn((B, n, Hkv, K), 17)
+    k[..., ::37] += 4.0
+    q = randn((B, Hq, K), 18)
+    check(mea, q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), lens, K ** -0.5, alibi)
