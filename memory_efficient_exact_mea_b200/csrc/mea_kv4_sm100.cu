@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
   // the dimensions of group gid / 4 alone.
   uint32_t qb[NG][4][2];
   float qsum[NT][2], scl[2];
+  bool wide;  // see `up` below; the same in the whole warp
   {
     const int head = PAIR ? gid & 3 : gid;
     const uint4* qrow = reinterpret_cast<const uint4*>(
@@ -603,9 +604,17 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
       for (int e = 0; e < 2; ++e) qsum[0][e] = __shfl_sync(0xffffffffu, col_sum, 8 * tig + 4 * e);
     }
+    // Scores y are kept in units of kUnitOdd, which goes into their scale (and out of the
+    // sums of q), so that s sum(q c) stays in range for any step; with a q so large (about
+    // 2^107) that its scale would leave the range, y takes it tile by tile.
+    wide = __any_sync(0xffffffffu, inv > 0x1p100f);
+    const float up = wide ? 1.f : kUnitOdd;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      scl[e] = __shfl_sync(0xffffffffu, inv, 8 * tig + 4 * e) * a.scale_log2;
+    for (int e = 0; e < 2; ++e) {
+      scl[e] = __shfl_sync(0xffffffffu, inv, 8 * tig + 4 * e) * up * a.scale_log2;
+#pragma unroll
+      for (int g = 0; g < NT; ++g) qsum[g][e] *= 1.f / kUnitOdd;
+    }
   }
   float slope[2] = {0.f, 0.f};
   if constexpr (ALIBI) {
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
-  // Scores of the tile in `slot` times the scale of q.
+  // Scores of the tile in `slot` times the scale of q, in units of kUnitOdd (`wide`: one).
   auto score = [&](int slot, float(&y)[2][4]) {
     const uint8_t* st = ring + slot * L::kStage;
     float sc[2][NT][4];
@@ -665,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
-          const float s = step_of<BF16>(kq[2 * blk + r][g]) * kUnitOdd;
+          const float s = step_of<BF16>(kq[2 * blk + r][g]);
           const float z = zero_of<BF16>(kq[2 * blk + r][g]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -679,6 +688,12 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[blk][e] += __shfl_xor_sync(0xffffffffu, y[blk][e], 2);
+    }
+    if (wide) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[blk][e] *= kUnitOdd;
     }
   };
 

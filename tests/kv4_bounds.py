@@ -56,7 +56,7 @@ def decode_bound(q, cache, lens, scale, alibi=False):
                 L = torch.logsumexp(x, 0)
                 p = torch.exp(x - L)
                 o = p @ v
-                second = math.exp(2 * float(e.amax()))
+                second = math.exp(min(2 * float(e.amax()), 600.0))
                 mag = p @ (15 * vs + vz)
                 held = (p @ (15 * vs)) * U.HELD[q.dtype] \
                     + 15 * n * 2.0 ** -28 * (p[:, None] * torch.maximum(vs, vz * 2.0 ** -12)).amax(0)

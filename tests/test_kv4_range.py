@@ -101,6 +101,31 @@ def test_equal_values_after_zeros(mea, K, Hq, z):
     check(mea, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n], K ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,mag", [("bf16", 1e33), ("bf16", 1e37), ("bf16", 1e-30),
+                                       ("bf16", 1e-36), ("f16", 1e4), ("f16", 1e-4)])
+@pytest.mark.parametrize("K,Hq", [(64, 2), (128, 3), (128, 6)])
+def test_keys_of_any_size(mea, dtype, mag, K, Hq):
+    """Keys near the ends of the type's range, q making up for it."""
+    n = 333
+    k, q = randn((2, n, 1, K), 21) * mag, randn((2, Hq, K), 22) / mag
+    v = randn((2, n, 1, K), 23)
+    check(mea, q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), [n, 60], K ** -0.5)
+    check(mea, q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), [n, 60], K ** -0.5, alibi=True)
+
+
+@pytest.mark.parametrize("K,Hq", [(64, 2), (128, 3), (128, 6)])
+def test_a_huge_query_leaves_the_other_heads_alone(mea, K, Hq):
+    n = 200
+    q, k, v = randn((1, Hq, K), 24), randn((1, n, 1, K), 25), randn((1, n, 1, K), 26)
+    q[:, 0] *= 1e35
+    q, k, v = q.bfloat16(), k.bfloat16(), v.bfloat16()
+    cache = filled(mea, k, v, [n])
+    out, lse = mea.mea_decode_kv4(q.to(DEV), cache, i32([n]), n)
+    (ro, rl), (eo, el) = decode_bound(q, [t.cpu() for t in cache], [n], K ** -0.5)
+    assert ((out.double().cpu() - ro).abs() <= eo)[:, 1:].all()
+    assert ((lse.double().cpu() - rl).abs() <= el)[:, 1:].all()
+
+
 PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
           4498, 4499]
 
