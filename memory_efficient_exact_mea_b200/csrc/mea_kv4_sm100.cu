@@ -434,7 +434,7 @@ struct KSmem {
   static constexpr int kStage = 2 * (kCodes + kParams);  // K codes, V codes, K params, V params
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kBytes = kWarps * kWarp;
-  // after the ring: ref, l [kWarps][kHeads], log2 of acc's unit [kWarps][kHeads][NG],
+  // after the ring: ref, l [kWarps][kHeads], log2 F [kWarps][kHeads][NG],
   // acc [kWarps][kHeads][D]
   static_assert(kWarps * kHeads * (D + 2 + NG) * 4 <= kBytes, "combine area");
 };
@@ -604,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
       for (int e = 0; e < 2; ++e) qsum[0][e] = __shfl_sync(0xffffffffu, col_sum, 8 * tig + 4 * e);
     }
-    // Scores y are kept in units of kUnitOdd, which goes into their scale (and out of the
+    // Scores are summed in units of kUnitOdd, which goes into their scale (and out of the
     // sums of q), so that s sum(q c) stays in range for any step; with a q so large (about
-    // 2^107) that its scale would leave the range, y takes it tile by tile.
+    // 2^107) that its scale would leave the range, they take it tile by tile.
     wide = __any_sync(0xffffffffu, inv > 0x1p100f);
     const float up = wide ? 1.f : kUnitOdd;
 #pragma unroll
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
-  // Scores of the tile in `slot` times the scale of q, in units of kUnitOdd (`wide`: one).
+  // Scores of the tile in `slot`, log2 units.
   auto score = [&](int slot, float(&y)[2][4]) {
     const uint8_t* st = ring + slot * L::kStage;
     float sc[2][NT][4];
@@ -689,6 +689,13 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[blk][e] += __shfl_xor_sync(0xffffffffu, y[blk][e], 2);
     }
+    // The scale is taken here and not together with the reference: the two roundings of
+    // y scl, here and in a fused y scl - ref, are 2^-24 y apart, which past scores of
+    // 2^24 is no longer a weight near one.
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[blk][e] *= scl[e & 1];
     if (wide) {
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       lds<4 * NT>(st + 2 * L::kCodes + L::kParams + (gid + 8 * i) * 4 * NG + 4 * own, vq[i]);
     const bool last = t + kTile > s1;
     if constexpr (ALIBI) {
-      // y scl - slope (n - 1 - row): y carries the bias in its own units
+      // y - slope (n - 1 - row)
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -720,10 +727,8 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
           y[blk][e] = fmaf(
               -slope[e & 1],
               static_cast<float>(n - 1 - min(t + 16 * blk + 8 * (e >> 1) + gid, s1 - 1)),
-              y[blk][e] * scl[e & 1]);
+              y[blk][e]);
     }
-    // log2 units: y itself under ALiBi, y scl otherwise
-    const float unit[2] = {ALIBI ? 1.f : scl[0], ALIBI ? 1.f : scl[1]};
     if (a.scores != nullptr) {  // kept for the gathered weights
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
                                       a.score_stride + t + gid;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (t + 8 * i + gid < s1) out[8 * i] = y[i >> 1][2 * (i & 1) + e] * unit[e];
+            if (t + 8 * i + gid < s1) out[8 * i] = y[i >> 1][2 * (i & 1) + e];
         }
     }
     // Weights of the tile against the present reference: p s F in fp16, and the sums
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
         float p[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          p[e] = ex2(fmaf(y[i >> 1][2 * (i & 1) + e], unit[e], -ref[e]));
+          p[e] = ex2(y[i >> 1][2 * (i & 1) + e] - ref[e]);
         if (last) {
           asm volatile("");  // a branch, not selects in every tile
           if (t + 8 * i + gid >= s1) p[0] = p[1] = 0.f;
@@ -793,23 +798,22 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
         };
         float v = neg_inf();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v = fmaxf(v, y[i >> 1][2 * (i & 1) + e] * unit[e]);
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, y[i >> 1][2 * (i & 1) + e]);
         const float r_new = fmaxf(ref[e], over_rows(v));
         const float drop = r_new == ref[e] ? 0.f : ref[e] - r_new;
         l_part[e] *= ex2(drop);
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
-          float m = neg_inf();  // log2 of the largest p s, against a reference of zero
+          float m = neg_inf();  // log2 of the largest p s against the new reference
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float mag = fmaxf(step_of<BF16>(vq[i][g]),
                                     fabsf(zero_of<BF16>(vq[i][g])) * 0x1p-12f);
-            m = fmaxf(m, y[i >> 1][2 * (i & 1) + e] * unit[e] + __log2f(mag));
+            m = fmaxf(m, (y[i >> 1][2 * (i & 1) + e] - r_new) + __log2f(mag));
           }
           const float f_old = log2_of(fac[g][e]);
-          m = fmaxf(over_rows(m), ref[e] + (kTarget - f_old));
-          const float f_new =
-              fminf(fmaxf(rintf(kTarget + (r_new - m)), kLeastFactor), kMostFactor);
+          m = fmaxf(over_rows(m), drop + (kTarget - f_old));
+          const float f_new = fminf(fmaxf(rintf(kTarget - m), kLeastFactor), kMostFactor);
           fac[g][e] = power_of_two(f_new);
           const float alpha = ex2(drop + (f_new - f_old));
           zacc[g][e] *= alpha;
@@ -879,8 +883,8 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
   __syncthreads();  // the rings are read: their memory joins the warps' states
   float* c_ref = reinterpret_cast<float*>(smem);
   float* c_l = c_ref + kWarps * kHeads;
-  float* c_unit = c_l + kWarps * kHeads;
-  float* c_acc = c_unit + kWarps * kHeads * NG;
+  float* c_fac = c_l + kWarps * kHeads;
+  float* c_acc = c_fac + kWarps * kHeads * NG;
   if (gid == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -890,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
         c_l[at] = l_part[e];
       }
 #pragma unroll
-      for (int g = 0; g < NT; ++g) c_unit[at * NG + own + g] = ref[e] - log2_of(fac[g][e]);
+      for (int g = 0; g < NT; ++g) c_fac[at * NG + own + g] = log2_of(fac[g][e]);
     }
   }
 #pragma unroll
@@ -905,22 +909,23 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
     const int g = idx / D, d = idx - g * D;
-    const float* units = c_unit + g * NG + d / 64;  // of warp w: units[w * kHeads * NG]
-    float mx = kNoRef, top = neg_inf();
+    float mx = kNoRef, top = neg_inf(), unit[kWarps];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      mx = fmaxf(mx, c_ref[w * kHeads + g]);
-      top = fmaxf(top, units[w * kHeads * NG]);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, c_ref[w * kHeads + g]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {  // log2 of what one of acc stands for, against mx
+      unit[w] = (c_ref[w * kHeads + g] - mx) - c_fac[(w * kHeads + g) * NG + d / 64];
+      top = fmaxf(top, unit[w]);
     }
     float lsum = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {  // factors of 1 if no warp has a reference
       lsum = fmaf(ex2(c_ref[w * kHeads + g] - mx), c_l[w * kHeads + g], lsum);
-      o = fmaf(ex2(units[w * kHeads * NG] - top), c_acc[(w * kHeads + g) * D + d], o);
+      o = fmaf(ex2(unit[w] - top), c_acc[(w * kHeads + g) * D + d], o);
     }
     const long long row = static_cast<long long>(b) * a.Hq + h0 + g;
-    // a NaN stays a NaN; the units' difference lies in -kMostFactor .. -kLeastFactor
-    const float val = lsum == 0.f ? 0.f : o / lsum * ex2(top - mx);
+    // (a NaN stays a NaN; top lies in -kMostFactor .. -kLeastFactor)
+    const float val = lsum == 0.f ? 0.f : o / lsum * ex2(top);
     const float lse2 = lsum == 0.f ? neg_inf() : mx + log2f(lsum);
     if (a.part_o == nullptr) {  // the only split
       static_cast<uint16_t*>(a.out)[row * D + d] = static_cast<uint16_t>(to_16<BF16>(val));

@@ -124,6 +124,30 @@ def test_a_huge_query_leaves_the_other_heads_alone(mea, K, Hq):
     (ro, rl), (eo, el) = decode_bound(q, [t.cpu() for t in cache], [n], K ** -0.5)
     assert ((out.double().cpu() - ro).abs() <= eo)[:, 1:].all()
     assert ((lse.double().cpu() - rl).abs() <= el)[:, 1:].all()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dtype,mag", [("f16", 3e2), ("f16", 6e4), ("bf16", 1e9), ("bf16", 1e15)])
+@pytest.mark.parametrize("K,Hq", [(64, 2), (128, 3), (128, 6)])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_scores_of_any_size(mea, dtype, mag, K, Hq, alibi):
+    """Scores far beyond 2^24: the largest takes all the weight."""
+    n = 300
+    k, v = randn((1, n, 1, K), 27), randn((1, n, 1, K), 28)
+    k[:, 177] = 4.0 * randn((K,), 29).sign()
+    q = k[:, None, 177, 0] * torch.linspace(1, 2, Hq).view(1, Hq, 1) / 8
+    k, q = (k * mag / 4).to(DT[dtype]), (q * mag).to(DT[dtype]).squeeze(1)
+    cache = filled(mea, k, v.to(DT[dtype]), [n])
+    out, lse = mea.mea_decode_kv4(q.to(DEV), cache, i32([n]), n, alibi=alibi)
+    (ro, rl), _ = decode_bound(q, [t.cpu() for t in cache], [n], K ** -0.5, alibi)
+    # the row's own values, one rounding; the scores' relative error for the lse
+    half, held = {"f16": (2.0 ** -11, 2.0 ** -21), "bf16": (2.0 ** -8, 2.0 ** -11)}[dtype]
+    row = mea.mea_kv4_read(cache, i32([n]))[1][0, 177, 0].double().cpu()
+    assert ((ro[0] - row).abs() <= row.abs() * half + 2.0 ** -25).all()
+    mag_v = cache.v_params[0, 0, 177].double().abs().cpu() @ torch.tensor([15.0, 1.0]).double()
+    tol = ro.abs() * half + mag_v.repeat_interleave(64) * (held + 2.0 ** -20)
+    assert ((out.double().cpu() - ro).abs() <= tol).all()
+    assert ((lse.double().cpu() - rl).abs() <= rl.abs() * K * 2.0 ** -21).all()
 
 
 PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
