@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 //
 // Both products run in fp16 whatever the input type.  q is scaled by a power of two to
 // a largest magnitude below 256, exact but for values 2^-22 of that and less.
-// P' = p s goes in as one fp16 number for bf16 results (11 bits against the result's
-// 8: the error against 64 bits stays at the result's own rounding) and as two, high
-// and low, for fp16 results (one would double their error).  p = 2^(y - ref) with ref
+// P' = p s goes in as two fp16 numbers, high and low (22 bits): with one, a fifth of the
+// bf16 results of the B = 64 decode differed from those of fp32 weights (2 % with two),
+// at 79 instead of 84 us.  p = 2^(y - ref) with ref
 // the running maximum of a head's scores; what goes in is p s F, F a power of two for
 // each (head, group of 64 dimensions) that puts the largest p s so far at 2^4, so that
 // a group keeps its bits however small its steps are beside the other group's.  fp16's
@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 // PAIR (K = 128, at most four heads): the columns that would be padding take the
 // second group of dimensions, so a thread works for one group only -- half the
 // arithmetic between the products (scores, p s, sums), one exchange of the scores'
-// halves.
+// halves.  In the product of a group's codes of V the other group's columns take this
+// group's low parts, so the low parts cost no product of their own.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -742,8 +743,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
     }
     // Weights of the tile against the present reference: p s F in fp16, and the sums
     // of p, p s F and p z F (an overflow shows in a sum of numbers >= 0).
-    constexpr int kParts = BF16 ? 1 : 2;
-    uint32_t pk[2][NT][2][kParts];
+    uint32_t pk[2][NT][2][2];  // [..][high, low]
     float sum[2], heavy[2], zsum[NT][2];
     auto weigh = [&] {
 #pragma unroll
@@ -771,10 +771,11 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
           heavy[1] += ps1;
           zsum[g][0] = fmaf(pf0, z, zsum[g][0]);
           zsum[g][1] = fmaf(pf1, z, zsum[g][1]);
-          uint32_t(&out)[kParts] = pk[i >> 1][g][i & 1];
+          uint32_t(&out)[2] = pk[i >> 1][g][i & 1];
           out[0] = pack2<false>(ps0, ps1);
-          if constexpr (kParts == 2)
-            out[1] = pack2<false>(ps0 - step_of<false>(out[0]), ps1 - zero_of<false>(out[0]));
+          constexpr uint16_t kMinusOne = 0xBC00;
+          out[1] = pack2<false>(fma_16<false>(static_cast<uint16_t>(out[0]), kMinusOne, ps0),
+                                fma_16<false>(static_cast<uint16_t>(out[0] >> 16), kMinusOne, ps1));
         }
         sum[0] += p[0];
         sum[1] += p[1];
@@ -816,13 +817,16 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
           const float f_new = fminf(fmaxf(rintf(kTarget - m), kLeastFactor), kMostFactor);
           fac[g][e] = power_of_two(f_new);
           const float alpha = ex2(drop + (f_new - f_old));
+          // PAIR: this thread's columns of the other group's products hold its low parts
+          const float other = PAIR ? __shfl_xor_sync(0xffffffffu, alpha, 2) : alpha;
           zacc[g][e] *= alpha;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            if (PAIR || (i >> 2) == g) {
-              acc[i][e] *= alpha;
-              acc[i][e + 2] *= alpha;
-            }
+          for (int i = 0; i < D / 16; ++i) {
+            if (!PAIR && (i >> 2) != g) continue;
+            const float by = PAIR && (i >> 2) != own ? other : alpha;
+            acc[i][e] *= by;
+            acc[i][e + 2] *= by;
+          }
         }
         ref[e] = r_new;
       }
@@ -835,18 +839,27 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
       zacc[g][0] += zsum[g][0];
       zacc[g][1] += zsum[g][1];
     }
-    uint32_t pb[2][NT][kParts][2];
+    // B operands of the products with V's codes.  PAIR: of a group, the high parts in its
+    // own columns and the low parts in the other's.
+    constexpr int kOps = PAIR ? 1 : 2;
+    uint32_t pb[2][NG][kOps][2];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-      for (int g = 0; g < NT; ++g)
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (PAIR) {
+          const uint32_t high = pk[blk][0][r][0];
+          const uint32_t low = __shfl_xor_sync(0xffffffffu, pk[blk][0][r][1], 2);
+          pb[blk][0][0][r] = movmatrix_trans(own == 0 ? high : low);
+          pb[blk][1][0][r] = movmatrix_trans(own == 0 ? low : high);
+        } else {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          pb[blk][g][part][0] = movmatrix_trans(pk[blk][g][0][part]);
-          pb[blk][g][part][1] = movmatrix_trans(pk[blk][g][1][part]);
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int op = 0; op < kOps; ++op)
+              pb[blk][g][op][r] = movmatrix_trans(pk[blk][g][r][op]);
         }
-    // PAIR: a group's dimensions against all columns; those of the other group are
-    // computed for nothing (they were the padding) and left out in the end
+      }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -864,9 +877,9 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
-            mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i],
-                        pb[blk][PAIR ? 0 : g][part][0], pb[blk][PAIR ? 0 : g][part][1]);
+          for (int op = 0; op < kOps; ++op)
+            mma_f16_acc(acc[4 * g + i], xa.n[i], ya.n[i], xb.n[i], yb.n[i], pb[blk][g][op][0],
+                        pb[blk][g][op][1]);
       }
     }
   }
@@ -900,11 +913,14 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)  // tile i: dimension 64 (i/4) + 8 gid + i % 4 (+ 4)
+    for (int e = 0; e < 4; ++e) {  // tile i: dimension 64 (i/4) + 8 gid + i % 4 (+ 4)
+      float x = acc[i][e];
+      if constexpr (PAIR) x += __shfl_xor_sync(0xffffffffu, x, 2);  // high and low parts
       if (!PAIR || own == (i >> 2))
         c_acc[(warp * kHeads + hp + (e & 1)) * D + 64 * (i >> 2) + 8 * gid + (i & 3) +
               4 * (e >> 1)] =
-            fmaf(acc[i][e], (i & 1) ? kUnitOdd : kUnitEven, zacc[PAIR ? 0 : i >> 2][e & 1]);
+            fmaf(x, (i & 1) ? kUnitOdd : kUnitEven, zacc[PAIR ? 0 : i >> 2][e & 1]);
+    }
   __syncthreads();
 
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {

@@ -7,8 +7,8 @@ order is covered by a factor exp(2 max e).
   e_j      K 2^-23 times scale sum |q| (15 s + |z|) of row j (K terms added in fp32, s q c
            and z q apart), 2^-22 of the score (its scaling and bias), 2^-21 for exp2 and
            for the joining of warps and splits by their references
-  held     p s as 16-bit numbers for the product: half a step each (kv4_util.HELD), and half
-           of fp16's least step, 2^-25, once the largest p s of the group in a warp's rows
+  held     p s as two fp16 numbers for the product: half a step of the second, 2^-22, or half
+           of fp16's least step, 2^-25, where the largest p s of the group in a warp's rows
            is put at 2^3 or more: at most 2^-28 of that largest p s a row
   sums     n terms in fp32, truncated: (n + 64) 2^-23 of the sum of p (15 s + |z|)
   result   half a step of its type, or of its least step below the normal range
@@ -21,6 +21,7 @@ import torch
 
 import kv4_util as U
 
+HELD = 2.0 ** -22
 LEAST = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}  # half the least step
 
 
@@ -58,7 +59,7 @@ def decode_bound(q, cache, lens, scale, alibi=False):
                 o = p @ v
                 second = math.exp(min(2 * float(e.amax()), 600.0))
                 mag = p @ (15 * vs + vz)
-                held = (p @ (15 * vs)) * U.HELD[q.dtype] \
+                held = (p @ (15 * vs)) * HELD \
                     + 15 * n * 2.0 ** -28 * (p[:, None] * torch.maximum(vs, vz * 2.0 ** -12)).amax(0)
                 lse[b, h], out[b, h] = L, o
                 e_lse[b, h] = (p @ e) * second + n * 2.0 ** -24 + L.abs() * 2.0 ** -23 + 2.0 ** -21

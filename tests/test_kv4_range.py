@@ -141,13 +141,26 @@ def test_scores_of_any_size(mea, dtype, mag, K, Hq, alibi):
     out, lse = mea.mea_decode_kv4(q.to(DEV), cache, i32([n]), n, alibi=alibi)
     (ro, rl), _ = decode_bound(q, [t.cpu() for t in cache], [n], K ** -0.5, alibi)
     # the row's own values, one rounding; the scores' relative error for the lse
-    half, held = {"f16": (2.0 ** -11, 2.0 ** -21), "bf16": (2.0 ** -8, 2.0 ** -11)}[dtype]
+    half, held = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype], 2.0 ** -21
     row = mea.mea_kv4_read(cache, i32([n]))[1][0, 177, 0].double().cpu()
     assert ((ro[0] - row).abs() <= row.abs() * half + 2.0 ** -25).all()
     mag_v = cache.v_params[0, 0, 177].double().abs().cpu() @ torch.tensor([15.0, 1.0]).double()
     tol = ro.abs() * half + mag_v.repeat_interleave(64) * (held + 2.0 ** -20)
     assert ((out.double().cpu() - ro).abs() <= tol).all()
     assert ((lse.double().cpu() - rl).abs() <= rl.abs() * K * 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("K,Hq", [(64, 2), (128, 2), (128, 6)])
+def test_equal_rows_give_that_row(mea, dtype, K, Hq):
+    """Rows of -8 .. 7 (step 1, zero -8, exact) at two scores whose weights are no short
+    numbers: the weights' bits cancel between the codes' sum and the zeros'."""
+    n = 40
+    v = (torch.arange(K) % 16 - 8.0).expand(1, n, 1, K)
+    q = randn((1, Hq, K), 31)
+    k = torch.zeros(1, n, 1, K)
+    k[:, 5] = q[:, :1] * 0.3
+    check(mea, q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), [n], K ** -0.5)
 
 
 PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
