@@ -335,7 +335,8 @@ int mea_bwd_stages(const void* q, const void* k, const void* v, const void* out,
  * and a code c stands for z + s c.  z is the group's least value, s its range / 15
  * (computed in fp32, rounded to the 16-bit type), c the nearest integer to
  * (x - z) / s, ties to even, held to 0..15; a group of equal values has s = 0 and
- * c = 0.  A group that holds a NaN or an infinity stands for NaN throughout.
+ * c = 0.  A group that holds a NaN or an infinity stands for NaN throughout.  Results
+ * that pass the type's largest number (z + 15 s may, by the rounding of s) are held to it.
  *
  * mea_kv4_append -- puts n = q_seqlens[b] (M if NULL) new rows of every sequence
  * after its past = cache_seqlens[b] rows, as mea_prefill_chunk does for a 16-bit
@@ -355,7 +356,7 @@ int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_
 
 /*
  * mea_kv4_read -- rows of a 4-bit cache as 16-bit rows (what the codes stand for,
- * rounded once), for the operations that take 16-bit keys and values: the history
+ * in fp32 and then rounded), for the operations that take 16-bit keys and values: the history
  * in front of a chunk of prefill, for instance.  For r < rows[b]:
  *     k_out[b, r] = cache row first_rows[b] + r (from row 0 if first_rows is NULL)
  *   k_out, v_out  [B, out_rows, Hkv, K] element strides (b, row, h), K contiguous;

@@ -233,6 +233,20 @@ __global__ void __launch_bounds__(kRowThreads, 5) kv4_append_kernel(const Kv4App
   }
 }
 
+// Results: rounded to 16 bits and held to the type's finite range (z + 15 s may pass it
+// by a step's rounding; an infinity is never stored), a NaN stays one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2_finite(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t to_16_finite(float x) {
+  return static_cast<uint16_t>(pack2_finite<BF16>(x, x));
+}
+
 // ---------------------------------------------------------------------------
 // Load: rows [first_b, first_b + count_b) of every head back into 16 bits.
 // ---------------------------------------------------------------------------
@@ -309,8 +323,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
     }
     if (u < rows)
       *reinterpret_cast<uint4*>(out + u * step) =
-          make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]),
-                     pack2<BF16>(v[6], v[7]));
+          make_uint4(pack2_finite<BF16>(v[0], v[1]), pack2_finite<BF16>(v[2], v[3]),
+                     pack2_finite<BF16>(v[4], v[5]), pack2_finite<BF16>(v[6], v[7]));
   }
 }
 
@@ -944,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 4 : 3) kv4_decode_kernel(cons
     const float val = lsum == 0.f ? 0.f : o / lsum * ex2(top);
     const float lse2 = lsum == 0.f ? neg_inf() : mx + log2f(lsum);
     if (a.part_o == nullptr) {  // the only split
-      static_cast<uint16_t*>(a.out)[row * D + d] = static_cast<uint16_t>(to_16<BF16>(val));
+      static_cast<uint16_t*>(a.out)[row * D + d] = to_16_finite<BF16>(val);
     } else {
       a.part_o[(row * a.max_splits + split) * D + d] = val;
     }
@@ -1009,7 +1023,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4DecodeArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      out[lane + 32 * i] = static_cast<uint16_t>(to_16<BF16>(o[i]));
+      out[lane + 32 * i] = to_16_finite<BF16>(o[i]);
     if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
     return;
   }

@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import kv4_util as U
 from kv4_bounds import decode_bound
 
 pytestmark = pytest.mark.gpu
@@ -161,6 +162,35 @@ def test_equal_rows_give_that_row(mea, dtype, K, Hq):
     k = torch.zeros(1, n, 1, K)
     k[:, 5] = q[:, :1] * 0.3
     check(mea, q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), [n], K ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_the_largest_numbers_stay_finite(mea, dtype):
+    """Groups that reach the type's largest number: z + 15 s passes it by the step's rounding,
+    and is held to it, read back or attended to; groups with a NaN or infinity stay NaN."""
+    dt = DT[dtype]
+    top = torch.finfo(dt).max
+    x = torch.zeros(8, 64)
+    x[0, 7] = top
+    x[1, 0], x[1, 1] = top, -top
+    x[2, 5] = -top
+    x[3] = top * (torch.arange(64) / 63.0)
+    x[4] = top * (torch.arange(64) / 31.5 - 1.0)
+    x[5, 9], x[6, 9], x[7, 9] = math.inf, -math.inf, math.nan
+    x = x.to(dt).reshape(8, 1, 1, 64).repeat(1, 1, 1, 2)
+    cache = filled(mea, x, x, [1] * 8)
+    want = U.values(*[t.cpu() for t in cache[:2]]).transpose(1, 2).clamp(-top, top)
+    k, v = mea.mea_kv4_read(cache, i32([1] * 8))
+    q = torch.zeros(8, 2, 128).to(dt).to(DEV)
+    out, _ = mea.mea_decode_kv4(q, cache, i32([1] * 8), 1)
+    out6, _ = mea.mea_decode_kv4(torch.zeros(8, 6, 128, dtype=dt, device=DEV), cache, i32([1] * 8), 1)
+    for got in (k, v, out[:, :1, None], out[:, 1:, None], out6[:, 5:, None]):
+        got = got.reshape(8, 1, 1, 128).double().cpu()
+        assert torch.isnan(got[5:]).all() and torch.isfinite(got[:5]).all()
+        tol = want.abs() * (U.HALF[dt] + 2.0 ** -20)
+        assert ((got - want).abs() <= tol)[:5].all()
+    # the listed top itself comes back
+    assert (k[0, 0, 0, 7] == top).item() and (k[1, 0, 0, 0] == top).item()
 
 
 PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
