@@ -434,17 +434,13 @@ def mea_decode(q, k_cache, v_cache, kv_seqstart, max_kv_len: int, scale: float |
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _launch(name, fn, index, stream, scratch, args):
-    """Runs fn(*args, stream) with CUDA device `index` current.  `scratch` are the tensors
-    this call allocated: on a stream that is not the one they were allocated for, their
-    memory may not be handed out again before the call has run."""
+def _launch(name, fn, index, stream, args):
+    """Runs fn(*args, stream) with CUDA device `index` current."""
     if stream is None:
         raw = _raw_stream(index) if _raw_stream is not None else \
             torch.cuda.current_stream(index).cuda_stream
     else:
         raw = stream.cuda_stream
-        for t in scratch:
-            t.record_stream(stream)
     if index == _current_device():
         rc = fn(*args, raw)
     else:
@@ -452,6 +448,27 @@ def _launch(name, fn, index, stream, scratch, args):
             rc = fn(*args, raw)
     if rc != 0:
         raise MeaError(name, rc)
+
+
+def _on_stream(index, stream):
+    """stream, if given, belongs to CUDA device `index`."""
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"stream must be a stream of cuda:{index}")
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """An uninitialised tensor for a call that runs on `stream` (None: the current one).  It
+    is allocated on that stream: memory freed on the current stream may still be in use by
+    work queued there, which nothing orders before the call.  If the caller gets it, its
+    current stream counts as a user of the memory too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and current != stream:
+        t.record_stream(current)
+    return t
 
 
 def _addr(t):
@@ -558,8 +575,9 @@ def mea_kv4_append(k_new, v_new, cache: Kv4Cache, cache_seqlens, q_seqlens=None,
     _on(index, v_new, "v_new")
     _lens(B, index, cache_seqlens, "cache_seqlens")
     _lens(B, index, q_seqlens, "q_seqlens")
+    _on_stream(index, stream)
     kc, kp, vc, vp = cache
-    _launch("mea_kv4_append", lib.mea_kv4_append, index, stream, (),
+    _launch("mea_kv4_append", lib.mea_kv4_append, index, stream,
             (k_new.data_ptr(), v_new.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(),
              vp.data_ptr(), cache_seqlens.data_ptr(), _addr(q_seqlens), B, M, rows, Hkv, K,
              _bmhk_strides(k_new, "k_new"), _bmhk_strides(v_new, "v_new"), _DTYPE[dtype]))
@@ -575,14 +593,12 @@ def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
     if out_rows is None:
         ref = k_out if k_out is not None else v_out
         out_rows = cap if ref is None else ref.shape[1]
-    fresh = []
+    _on_stream(index, stream)
     shape = (B, int(out_rows), Hkv, K)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
-        fresh.append(k_out)
+        k_out = _empty(shape, dtype, cache.k_codes.device, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
-        fresh.append(v_out)
+        v_out = _empty(shape, dtype, cache.k_codes.device, stream)
     if k_out.shape != shape or v_out.shape != shape or k_out.dtype != dtype \
             or v_out.dtype != dtype:
         raise ValueError(f"k_out and v_out must be {list(shape)} of the params' dtype")
@@ -591,7 +607,7 @@ def mea_kv4_read(cache: Kv4Cache, rows, first_rows=None, k_out=None, v_out=None,
     _lens(B, index, rows, "rows")
     _lens(B, index, first_rows, "first_rows")
     kc, kp, vc, vp = cache
-    _launch("mea_kv4_read", lib.mea_kv4_read, index, stream, fresh,
+    _launch("mea_kv4_read", lib.mea_kv4_read, index, stream,
             (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), rows.data_ptr(),
              _addr(first_rows), k_out.data_ptr(), v_out.data_ptr(), B, cap, shape[1], Hkv, K,
              _bmhk_strides(k_out, "k_out"), _bmhk_strides(v_out, "v_out"), _DTYPE[dtype]))
@@ -626,27 +642,25 @@ def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float
     if q.dtype != dtype:
         raise ValueError("q must have the dtype of the cache's params")
     scale = K ** -0.5 if scale is None else float(scale)
-    max_kv_len, fresh = int(max_kv_len), []
+    max_kv_len = int(max_kv_len)
+    _on(index, q, "q")
+    _on_stream(index, stream)
     if out is None:
-        out = torch.empty_like(q)
-        fresh.append(out)
+        out = _empty(shape, dtype, q.device, stream)
     elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped and typed like q")
     if lse is not None:
         _f32(lse, (B, Hq), index, "lse")
     elif return_lse:
-        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
-        fresh.append(lse)
+        lse = _empty((B, Hq), _F32, q.device, stream)
     want = return_weights or weights_out is not None
     if weights is not None and not want:
         raise ValueError("weights needs return_weights or weights_out")
     if want:
         if weights_out is None:
-            weights_out = torch.empty((B, Hkv, cap), dtype=_F32, device=q.device)
-            fresh.append(weights_out)
+            weights_out = _empty((B, Hkv, cap), _F32, q.device, stream)
         _f32(weights, (B, Hkv, cap), index, "weights")
         _f32(weights_out, (B, Hkv, cap), index, "weights_out")
-    _on(index, q, "q")
     _on(index, out, "out")
     _on(index, workspace, "workspace")
     _lens(B, index, kv_seqlens, "kv_seqlens")
@@ -654,14 +668,13 @@ def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float
     if workspace is None:
         need = mea_decode_kv4_workspace_size(B, Hq, Hkv, K, max_kv_len, want)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            fresh.append(workspace)
+            workspace = _empty(need, _U8, q.device, stream, returned=False)
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         ws_bytes = workspace.numel() * workspace.element_size()
     kc, kp, vc, vp = cache
-    _launch("mea_decode_kv4", lib.mea_decode_kv4, index, stream, fresh,
+    _launch("mea_decode_kv4", lib.mea_decode_kv4, index, stream,
             (q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
              kv_seqlens.data_ptr(), out.data_ptr(), _addr(lse), _addr(weights),
              _addr(weights_out), B, Hq, Hkv, K, cap, max_kv_len, _DTYPE[dtype],
@@ -692,17 +705,16 @@ def mea_key_weights(q, k, lse, cache_seqlens=None, q_seqlens=None, causal: bool 
         raise ValueError("lse must be what the attention of these queries returned")
     scale = K ** -0.5 if scale is None else float(scale)
     index = _cuda_index(q, "q")
-    fresh = []
+    _on_stream(index, stream)
     if out is None:
-        out = torch.empty((B, Hkv, N), dtype=_F32, device=q.device)
-        fresh.append(out)
+        out = _empty((B, Hkv, N), _F32, q.device, stream)
     _f32(lse, (B, Hq, M), index, "lse")
     _f32(weights, (B, Hkv, N), index, "weights")
     _f32(out, (B, Hkv, N), index, "out")
     _on(index, k, "k")
     _lens(B, index, cache_seqlens, "cache_seqlens")
     _lens(B, index, q_seqlens, "q_seqlens")
-    _launch("mea_key_weights", lib.mea_key_weights, index, stream, fresh,
+    _launch("mea_key_weights", lib.mea_key_weights, index, stream,
             (q.data_ptr(), k.data_ptr(), lse.data_ptr(), _addr(cache_seqlens), _addr(q_seqlens),
              _addr(weights), out.data_ptr(), B, M, N, Hq, Hkv, K, _bmhk_strides(q, "q"),
              _bmhk_strides(k, "k"), _DTYPE[q.dtype], 1 if causal else 0, 1 if alibi else 0,
@@ -758,16 +770,14 @@ def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out
         if out_index != index:
             raise ValueError(f"out must lie on cuda:{index}")
     budget, recent = int(budget), int(recent)
-    dev, fresh = src[0][0].device, []
+    dev = src[0][0].device
+    _on_stream(index, stream)
     if weights_out is None:
-        weights_out = torch.empty((B, Hkv, out_rows), dtype=torch.float32, device=dev)
-        fresh.append(weights_out)
+        weights_out = _empty((B, Hkv, out_rows), _F32, dev, stream)
     if new_seqlens is None:
-        new_seqlens = torch.empty(B, dtype=torch.int32, device=dev)
-        fresh.append(new_seqlens)
+        new_seqlens = _empty((B,), _I32, dev, stream)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
-        fresh.append(kept)
+        kept = _empty((B, Hkv, max(budget, 0)), _I32, dev, stream)
     _f32(weights, (B, Hkv, rows), index, "weights")
     _f32(weights_out, (B, Hkv, out_rows), index, "weights_out")
     if kept.dtype is not _I32 or kept.shape != (B, Hkv, budget) or not kept.is_contiguous():
@@ -784,7 +794,7 @@ def mea_cache_evict(cache, weights, cache_seqlens, budget: int, recent: int, out
         plane.src_strides = _byte_strides(s.stride(), size, r, h)
         plane.dst_strides = plane.src_strides if d is s else _byte_strides(d.stride(), size, r, h)
         plane.row_bytes = s.shape[3:].numel() * size
-    _launch("mea_cache_evict", lib.mea_cache_evict, index, stream, fresh,
+    _launch("mea_cache_evict", lib.mea_cache_evict, index, stream,
             (planes, len(src), weights.data_ptr(), weights_out.data_ptr(),
              cache_seqlens.data_ptr(), new_seqlens.data_ptr(), kept.data_ptr(), B, Hkv, rows,
              out_rows, budget, recent))
