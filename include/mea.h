@@ -451,8 +451,9 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
  *                after the last
  * In place: dst == src with the same strides, weights_out == weights, out_rows ==
  * cache_rows; or into other memory: no destination may overlap a source otherwise
- * (MEA_ERR_INVALID_ARG), nor two planes' destinations each other (interleaved rows of
- * one array are fine).  out_rows >= budget >= 1, 0 <= recent <= budget.  Destination
+ * (MEA_ERR_INVALID_ARG), nor two rows of destinations each other (a destination's strides
+ * nest; two planes whose destinations lie within one another have the same strides, as
+ * interleaved rows of one array do), nor kept or new_seqlens anything.  out_rows >= budget >= 1, 0 <= recent <= budget.  Destination
  * rows past the kept ones are left as they were.  A sequence with n outside
  * [0, cache_rows] is not moved: new_seqlens 0, kept -1, MEA_ERR_INVALID_ARG in the
  * device status word.

@@ -20,6 +20,67 @@ bool strides_ok(const int64_t s[3]) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// ---------------------------------------------------------------------------
+// Where outputs may lie.  Blocks write rows in no order, so two rows of outputs in one
+// place would leave whichever came last.
+// ---------------------------------------------------------------------------
+bool ranges_meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uint8_t *p = static_cast<const uint8_t*>(a), *q = static_cast<const uint8_t*>(b);
+  return p < q + b_bytes && q < p + a_bytes;
+}
+
+// Rows of `bytes` bytes at base + sum of i_k step_k: the axes longer than one, longest step
+// first, and the bytes from the first row to the last one's end.
+struct RowSet {
+  const uint8_t* base = nullptr;
+  int64_t n[3], step[3], bytes = 0, extent = 0;
+  int axes = 0;
+};
+
+// False if rows meet one another (a step shorter than what it steps over) or lie too far
+// apart for the arithmetic below.
+bool row_set(RowSet* r, const void* base, const int64_t n[3], const int64_t step[3],
+             int64_t bytes) {
+  r->base = static_cast<const uint8_t*>(base);
+  r->bytes = r->extent = bytes;
+  for (int k = 0; k < 3; ++k) {
+    if (n[k] <= 1) continue;
+    int at = r->axes++;
+    for (; at > 0 && r->step[at - 1] < step[k]; --at) {
+      r->step[at] = r->step[at - 1];
+      r->n[at] = r->n[at - 1];
+    }
+    r->step[at] = step[k];
+    r->n[at] = n[k];
+  }
+  for (int k = r->axes - 1; k >= 0; --k) {
+    if (r->step[k] < r->extent || r->n[k] - 1 > (int64_t(1) << 60) / r->step[k]) return false;
+    r->extent += (r->n[k] - 1) * r->step[k];
+    if (r->extent > int64_t(1) << 60) return false;
+  }
+  return true;
+}
+
+// Whether a row of b, which begins `apart` bytes after a's row with the same indices, meets
+// a row of a in the axes from k on.  The rest of the axes spans less than one step, so only
+// the two nearest steps can bring them together.
+bool rows_meet(const RowSet& a, const RowSet& b, int64_t apart, int k) {
+  if (k == a.axes) return apart < a.bytes && -apart < b.bytes;
+  const int64_t i = apart >= 0 ? apart / a.step[k] : -((-apart + a.step[k] - 1) / a.step[k]);
+  for (const int64_t j : {i, i + 1})
+    if (j < a.n[k] && -j < a.n[k] && rows_meet(a, b, apart - j * a.step[k], k + 1)) return true;
+  return false;
+}
+
+// True if rows of a and b meet, or if their steps differ and they lie within one another.
+bool sets_meet(const RowSet& a, const RowSet& b) {
+  if (!ranges_meet(a.base, a.extent, b.base, b.extent)) return false;
+  if (a.axes != b.axes) return true;
+  for (int k = 0; k < a.axes; ++k)
+    if (a.n[k] != b.n[k] || a.step[k] != b.step[k]) return true;
+  return rows_meet(a, b, b.base - a.base, 0);
+}
+
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int kMaxLen = 1 << 30;  // rows of one sequence: tile arithmetic stays in 32 bits
 
@@ -300,13 +361,6 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
   return mea::launch_weights(L, stream) == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
 }
 
-// First byte past the rows an array of `rows` x Hkv x B rows touches.
-static const uint8_t* plane_end(const void* p, const int64_t st[3], int B, int rows, int Hkv,
-                                int row_bytes) {
-  return static_cast<const uint8_t*>(p) + st[0] * (B - 1) + st[1] * (rows - 1) +
-         st[2] * (Hkv - 1) + row_bytes;
-}
-
 int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weights,
                     float* weights_out, const int32_t* cache_seqlens, int32_t* new_seqlens,
                     int32_t* kept, int B, int Hkv, int cache_rows, int out_rows, int budget,
@@ -364,21 +418,46 @@ int mea_cache_evict(const mea_plane_t* planes, int n_planes, const float* weight
       in_place = true;
     }
   }
+  // Destinations: the planes', each row in a place of its own (the rows of several planes
+  // of one array may interleave), away from every source but, in place, their own and
+  // those cut in place with it.
+  RowSet dst[mea::kMaxPlanes];
+  const uint8_t *s0[mea::kMaxPlanes], *s1[mea::kMaxPlanes];  // what the sources span
+  const int64_t dst_n[3] = {B, out_rows, Hkv}, src_n[3] = {B, cache_rows, Hkv};
+  for (int p = 0; p < total; ++p) {
+    if (!row_set(&dst[p], all[p].dst, dst_n, all[p].dst_strides, all[p].row_bytes))
+      return MEA_ERR_INVALID_ARG;
+    int64_t span = all[p].row_bytes;
+    for (int i = 0; i < 3; ++i) {
+      const int64_t step = all[p].src_strides[i];
+      if (step > 0 && src_n[i] - 1 > (int64_t(1) << 60) / step) return MEA_ERR_INVALID_ARG;
+      span += (src_n[i] - 1) * step;
+    }
+    s0[p] = a.planes[p].src;
+    s1[p] = s0[p] + span;
+  }
   for (int d = 0; d < total; ++d)
     for (int s = 0; s < total; ++s) {
-      if (d == s && all[d].src == all[d].dst) continue;
-      const uint8_t* d0 = a.planes[d].dst;
-      const uint8_t* d1 = plane_end(d0, all[d].dst_strides, B, out_rows, Hkv, all[d].row_bytes);
-      const uint8_t* s0 = a.planes[s].src;
-      const uint8_t* s1 = plane_end(s0, all[s].src_strides, B, cache_rows, Hkv, all[s].row_bytes);
-      // planes of one cache may interleave (a key and a value view of one array)
+      if (d < s && sets_meet(dst[d], dst[s])) return MEA_ERR_INVALID_ARG;
       const bool same_array = all[d].src == all[d].dst && all[s].src == all[s].dst;
-      if (!same_array && d0 < s1 && s0 < d1) return MEA_ERR_INVALID_ARG;
-      // two planes written to the same rows
-      const uint8_t* e0 = a.planes[s].dst;
-      const int64_t apart = d0 < e0 ? e0 - d0 : d0 - e0;
-      if (d < s && apart < (d0 < e0 ? all[d] : all[s]).row_bytes) return MEA_ERR_INVALID_ARG;
+      if (!same_array && ranges_meet(dst[d].base, dst[d].extent, s0[s], s1[s] - s0[s]))
+        return MEA_ERR_INVALID_ARG;
     }
+  // kept and new_seqlens: away from all of these, and from the lengths
+  const int64_t kept_bytes = static_cast<int64_t>(B) * Hkv * budget * 4, len_bytes = int64_t(4) * B;
+  if (ranges_meet(kept, kept_bytes, new_seqlens, len_bytes) ||
+      ranges_meet(kept, kept_bytes, cache_seqlens, len_bytes) ||
+      ranges_meet(new_seqlens, len_bytes, cache_seqlens, len_bytes))
+    return MEA_ERR_INVALID_ARG;
+  for (int p = 0; p < total; ++p) {
+    const int64_t span = s1[p] - s0[p];
+    if (ranges_meet(kept, kept_bytes, dst[p].base, dst[p].extent) ||
+        ranges_meet(kept, kept_bytes, s0[p], span) ||
+        ranges_meet(new_seqlens, len_bytes, dst[p].base, dst[p].extent) ||
+        ranges_meet(new_seqlens, len_bytes, s0[p], span) ||
+        ranges_meet(cache_seqlens, len_bytes, dst[p].base, dst[p].extent))
+      return MEA_ERR_INVALID_ARG;
+  }
 
   // Blocks: (column piece of a plane) x (sequence, kv head) x row segment.  Into
   // other memory the rows are shared out; in place a piece's rows are one block's,
