@@ -344,7 +344,8 @@ int mea_bwd_stages(const void* q, const void* k, const void* v, const void* out,
  *   k_new, v_new  [B, M, Hkv, K] element strides (b, m, h), K contiguous; rows >= n unused
  *   cache_seqlens DEVICE int32 [B], not updated (the caller adds n afterwards)
  * A sequence with past < 0, n outside [0, M] or past + n > cache_rows is skipped
- * and records MEA_ERR_INVALID_ARG in the device status word.  Here and below, a
+ * and records MEA_ERR_INVALID_ARG in the device status word.  No plane may overlap another
+ * (MEA_ERR_INVALID_ARG).  Here and below, a
  * sequence of more than 2^30 rows or a batch of 2^31 rows x heads returns
  * MEA_ERR_UNSUPPORTED.
  */
@@ -360,7 +361,8 @@ int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_
  * in front of a chunk of prefill, for instance.  For r < rows[b]:
  *     k_out[b, r] = cache row first_rows[b] + r (from row 0 if first_rows is NULL)
  *   k_out, v_out  [B, out_rows, Hkv, K] element strides (b, row, h), K contiguous;
- *                 rows >= rows[b] are not written
+ *                 rows >= rows[b] are not written; no two rows in one place
+ *                 (MEA_ERR_INVALID_ARG; interleaved rows of one array are fine)
  *   rows, first_rows  DEVICE int32 [B]; rows[b] outside [0, out_rows] or a range
  *                 outside the cache: the sequence is skipped, MEA_ERR_INVALID_ARG
  *                 in the device status word.
@@ -385,7 +387,8 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
  *                weights_out[b, h, j] = weights_in[b, h, j] + sum of softmax weights of
  *                row j over the query heads of kv head h, for j < kv_seqlens[b], and 0
  *                for the rows after them
- *   weights_in   the same layout, may be weights_out itself; NULL counts as zeros
+ *   weights_in   the same layout, may be weights_out itself, but not overlap it
+ *                otherwise (MEA_ERR_INVALID_ARG); NULL counts as zeros
  * Any group size Hq / Hkv.  ALiBi as in mea_decode (position = row number; rows that
  * mea_cache_evict has moved count from where they are now).  An empty
  * sequence gives out = 0, lse = -inf.  A sequence whose length is negative or above
@@ -421,7 +424,7 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
  *        take part and past = N - M (mea_fwd); q_seqlens must then be NULL.
  *   causal  0 or 1: row i sees keys j <= past + i
  *   weights_in, weights_out  [B, Hkv, N] fp32 contiguous; weights_in may be weights_out
- *        itself, NULL counts as zeros.  Rows past + n and later get 0.
+ *        itself, but not overlap it otherwise (MEA_ERR_INVALID_ARG); NULL counts as zeros.  Rows past + n and later get 0.
  * A sequence with past < 0, n outside [0, M] or past + n > N is skipped (weights_out
  * left as it was) and records MEA_ERR_INVALID_ARG in the device status word; a bounded
  * wait that gives up records MEA_ERR_DEVICE_TIMEOUT and leaves NaN in its keys' weights.

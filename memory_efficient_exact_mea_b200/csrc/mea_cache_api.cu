@@ -148,6 +148,13 @@ int mea_kv4_append(const void* k_new, const void* v_new, void* k_codes, void* k_
   if (!strides_ok(kn_strides) || !strides_ok(vn_strides)) return MEA_ERR_UNSUPPORTED;
   mea::Kv4AppendArgs a{};
   if (!row_order(&a.order, B, M, Hkv)) return MEA_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(B) * Hkv * cache_rows;
+  const void* planes[4] = {k_codes, v_codes, k_params, v_params};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (ranges_meet(planes[i], rows * (i < 2 ? K / 2 : K / 16), planes[j],
+                      rows * (j < 2 ? K / 2 : K / 16)))
+        return MEA_ERR_INVALID_ARG;
   a.k_new = k_new;
   a.v_new = v_new;
   a.k_codes = k_codes;
@@ -188,6 +195,13 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
   if (!strides_ok(ko_strides) || !strides_ok(vo_strides)) return MEA_ERR_UNSUPPORTED;
   mea::Kv4ReadArgs a{};
   if (!row_order(&a.order, B, out_rows, Hkv)) return MEA_ERR_UNSUPPORTED;
+  const int64_t n[3] = {B, out_rows, Hkv};
+  const int64_t ko[3] = {2 * ko_strides[0], 2 * ko_strides[1], 2 * ko_strides[2]};
+  const int64_t vo[3] = {2 * vo_strides[0], 2 * vo_strides[1], 2 * vo_strides[2]};
+  RowSet kr, vr;
+  if (!row_set(&kr, k_out, n, ko, 2 * K) || !row_set(&vr, v_out, n, vo, 2 * K) ||
+      sets_meet(kr, vr))
+    return MEA_ERR_INVALID_ARG;
   a.k_codes = k_codes;
   a.k_params = k_params;
   a.v_codes = v_codes;
@@ -257,6 +271,10 @@ int mea_decode_kv4(const void* q, const void* k_codes, const void* k_params, con
   if (need > 0 && (!workspace || workspace_bytes < need ||
                    (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return MEA_ERR_WORKSPACE;
+  const int64_t weight_bytes = static_cast<int64_t>(B) * Hkv * cache_rows * 4;
+  if (weights_in && weights_in != weights_out &&
+      ranges_meet(weights_in, weight_bytes, weights_out, weight_bytes))
+    return MEA_ERR_INVALID_ARG;
   mea::Kv4DecodeArgs a{};
   const DecodePlan p = decode_plan(B, Hq, Hkv, max_kv_len);
   if (static_cast<int64_t>(Hkv) * p.head_blocks > 65535 || B > 65535) return MEA_ERR_UNSUPPORTED;
@@ -320,6 +338,10 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
   if (!strides_ok(q_strides) || !strides_ok(k_strides)) return MEA_ERR_UNSUPPORTED;
   const int64_t blocks = (static_cast<int64_t>(N) + mea::kWeightKeys - 1) / mea::kWeightKeys;
   if (static_cast<int64_t>(B) * Hkv > kMaxRows / blocks) return MEA_ERR_UNSUPPORTED;
+  const int64_t weight_bytes = static_cast<int64_t>(B) * Hkv * N * 4;
+  if (weights_in && weights_in != weights_out &&
+      ranges_meet(weights_in, weight_bytes, weights_out, weight_bytes))
+    return MEA_ERR_INVALID_ARG;
   mea::WeightLaunch L{};
   mea::WeightArgs& a = L.args;
   a.status = mea::device_status_word();

@@ -1,11 +1,11 @@
-"""Where an eviction's outputs may lie: two rows of outputs in one place, or an output over
-an input, is refused on the host; interleaved rows of one array are not."""
+"""Where the cache operators' outputs may lie: two rows of outputs in one place, or an output
+over an input, is refused on the host; interleaved rows of one array are not."""
 import pytest
 import torch
 
 import kv4_util as U
 import memory_efficient_exact_mea_b200 as m
-from test_cache_ops_host import I64, INVALID, P, evict
+from test_cache_ops_host import APPEND, DECODE, I64, INVALID, P, READ, WEIGH, call, evict
 
 M24, M25 = 1 << 24, 1 << 25
 
@@ -40,6 +40,28 @@ def test_evict_in_place():
             p[i] = m._Plane(at, at, I64(320, 32, 16), I64(320, 32, 16), 16)
         assert m.lib.mea_cache_evict(p, 2, P(1 << 20), P(1 << 20), P(16), P(64), P(4096), 2, 2, 10,
                                      10, 5, 1, None) == INVALID
+
+
+@pytest.mark.parametrize("fn,base,kw", [
+    ("mea_kv4_append", APPEND, dict()),                   # all planes at one address
+    ("mea_kv4_append", APPEND, dict(kc=P(M24), kp=P(M25), vc=P(M24 + 512), vp=P(1 << 26))),
+    ("mea_kv4_append", APPEND, dict(kc=P(M24), kp=P(M24 + 624), vc=P(M25), vp=P(1 << 26))),
+    ("mea_kv4_append", APPEND, dict(kc=P(M24), kp=P(M25), vc=P(1 << 26), vp=P(M25 + 64))),
+    # rows [2, 5, 1] of 128 bytes
+    ("mea_kv4_read", READ, dict()),
+    ("mea_kv4_read", READ, dict(k=P(M24), v=P(M24 + 128))),
+    ("mea_kv4_read", READ, dict(k=P(M24), v=P(M24 + 2048))),
+    ("mea_kv4_read", READ, dict(k=P(M24), v=P(M24 + 16))),
+    ("mea_kv4_read", READ, dict(k=P(M24), v=P(M25), ks=I64(1024, 32, 64))),
+    ("mea_kv4_read", READ, dict(k=P(M24), v=P(M25), vs=I64(64, 64, 64))),
+    # weights [2, 2, 100] and [2, 2, 9]
+    ("mea_decode_kv4", DECODE, dict(win=P(M24), wout=P(M24 + 4))),
+    ("mea_decode_kv4", DECODE, dict(win=P(M24 + 1596), wout=P(M24))),
+    ("mea_key_weights", WEIGH, dict(win=P(M24), wout=P(M24 + 140))),
+    ("mea_key_weights", WEIGH, dict(win=P(M24 + 36), wout=P(M24))),
+])
+def test_others(fn, base, kw):
+    assert call(getattr(m.lib, fn), base, **kw) == INVALID
 
 
 VIEWS = {  # [B, rows, H, K] views of one array for keys and values, side by side
@@ -77,4 +99,10 @@ def test_interleaved_arrays_are_taken(kind, B, H):
                 for got, rest in ((dst[i].cpu(), old[i]), (src[i].cpu(), before[i])):
                     assert torch.equal(got[b, :budget, h], before[i][b, rows, h])
                     assert torch.equal(got[b, budget:, h], rest[b, budget:, h])
+    cache = m.mea_kv4_alloc(B, n, H, K, torch.float16)
+    m.mea_kv4_append(src[0][:, :n], src[1][:, :n], cache, torch.zeros_like(lens))
+    want = m.mea_kv4_read(cache, lens)
+    m.mea_kv4_read(cache, lens, k_out=src[0], v_out=src[1])
+    for i in range(2):
+        assert torch.equal(src[i][:, :n], want[i])
     assert m.read_device_status() == 0
