@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "mea.h"
+#include "mea_cache_internal.h"
 #include "mea_internal.h"
 #include "sm100.cuh"
 

@@ -6,7 +6,7 @@
 #include <algorithm>
 
 #include "mea.h"
-#include "mea_internal.h"
+#include "mea_cache_internal.h"
 
 namespace {
 

@@ -16,7 +16,7 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include "mea_internal.h"
+#include "mea_cache_internal.h"
 #include "sm100.cuh"
 
 namespace mea {

@@ -11,7 +11,7 @@
 // beyond |z + s c - x| <= s/2 (and 15 half steps of s's rounding at c = 15).
 #include <math.h>
 
-#include "mea_internal.h"
+#include "mea_cache_internal.h"
 #include "sm100.cuh"
 
 namespace mea {

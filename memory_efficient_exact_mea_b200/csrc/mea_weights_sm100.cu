@@ -20,7 +20,7 @@
 
 #include <type_traits>
 
-#include "mea_internal.h"
+#include "mea_cache_internal.h"
 #include "sm100.cuh"
 
 namespace mea {

@@ -413,12 +413,6 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Waits until the kernels before this one in the stream have finished and their
-// writes can be read (a kernel launched with launch_after).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------
 // Small arithmetic helpers
 // ---------------------------------------------------------------------------
