@@ -94,7 +94,8 @@ struct WCfg {
   static constexpr int kQ = kHalves * kKTile;
   static constexpr int kLse = kQ + kStages * kQTile;      // [slot][NQ] -lse * log2(e)
   static constexpr int kSlope = kLse + kLseSlots * NQ * 4;  // [slot] the tile's ALiBi slope
-  static constexpr int kSum = kSlope + kLseSlots * 4;      // [kKeys]
+  static constexpr int kOpen = kSlope + kLseSlots * 4;     // [slot] every row takes weight
+  static constexpr int kSum = kOpen + kLseSlots * 4;       // [kKeys]
   static constexpr int kPart = kSum + kKeys * 4;           // [kMaxWeightParts][kKeys]
   static constexpr int kBar = kPart + kMaxWeightParts * kKeys * 4;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kLseSlots + 4 * kHalves;
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
   uint64_t* mma_done = s_free + 2 * C::kHalves;
   float* s_lse = reinterpret_cast<float*>(smem + C::kLse);
   float* s_slope = reinterpret_cast<float*>(smem + C::kSlope);
+  int* s_open = reinterpret_cast<int*>(smem + C::kOpen);
   float* s_sum = reinterpret_cast<float*>(smem + C::kSum);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbort);
@@ -222,9 +224,15 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
       }
       ++issued;
       if (!mbar_wait_warp(&l_empty[ls], ((s / C::kLseSlots) & 1) ^ 1, abort_flag, a.status)) break;
+      bool open = true;
 #pragma unroll
-      for (int u = 0; u < NQ / 32; ++u)  // -inf: the row takes no weight
-        s_lse[ls * NQ + u * 32 + lane] = l2[u] == neg_inf() ? l2[u] : -l2[u] * kLog2e;
+      for (int u = 0; u < NQ / 32; ++u) {  // -inf: the row takes no weight
+        const float nl = l2[u] == neg_inf() ? l2[u] : -l2[u] * kLog2e;
+        s_lse[ls * NQ + u * 32 + lane] = nl;
+        open = open && nl != neg_inf();
+      }
+      open = __all_sync(0xffffffffu, open);
+      if (lane == 0) s_open[ls] = open;
       if (ALIBI && lane == 0)
         s_slope[ls] = exp2f(-8.0f * static_cast<float>(h + 1) / a.Hq) * kLog2e;
       mbar_arrive_warp(&l_full[ls]);
@@ -274,15 +282,15 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
       const int ls = s % C::kLseSlots, buf = 2 * half + (s & 1);
       // row i = m0 + row(c) sees this key iff i >= key - past
       const int first = CAUSAL ? max(0, key - past - m0) : 0;
-      const bool whole = m0 + NQ <= m &&
-                         (!CAUSAL || n0 + (half + 1) * kWeightKeys - 1 - past <= m0);
+      const bool seen = !CAUSAL || n0 + (half + 1) * kWeightKeys - 1 - past <= m0;
       if (!mbar_wait_warp(&l_full[ls], (s / C::kLseSlots) & 1, abort_flag, a.status) ||
           !mbar_wait_warp(&s_full[buf], (s >> 1) & 1, abort_flag, a.status))
         break;
       tc_fence_after();
       const float* lse = s_lse + ls * NQ;
       [[maybe_unused]] const float slope = ALIBI ? s_slope[ls] : 0.f;
-      // `open`: every column of the tile counts for every key of it
+      // `open`: every column of the tile counts for every key of it (rows past m have an
+      // lse of -inf here; a row that takes no weight may hold anything, NaN too)
       auto add_tile = [&](auto open) {
 #pragma unroll 2
         for (int c0 = 0; c0 < NQ; c0 += 32) {
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
           }
         }
       };
-      if (whole) add_tile(std::true_type{});
+      if (seen && s_open[ls]) add_tile(std::true_type{});
       else add_tile(std::false_type{});
       mbar_arrive_warp(&l_empty[ls]);
     }
