@@ -36,11 +36,12 @@ __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); 
 // acc + 2^x for a pair, on the FMA pipe: 2^x = 2^n 2^f with n the integer next to x
 // (added into the low mantissa bits of 1.5 2^23) and 2^f, |f| <= 1/2, by a polynomial
 // of degree 5 fitted here for the least relative error (7.5e-8; 2.2e-7 with fp32's
-// roundings).  x <= -126.5 gives 0, x >= 127 stays there, a NaN stays a NaN.
+// roundings).  x < -126.5 gives 0, x > 127.5 infinity (2^n is then no number; exp2 itself
+// ends half a step later), a NaN stays a NaN.
 __device__ __forceinline__ float clamp_exponent(float x) {
   float y;
   asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(y) : "f"(x));  // -127
-  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(y) : "f"(y));  // 127
+  asm("min.NaN.f32 %0, %1, 0f43000000;" : "=f"(y) : "f"(y));  // 128
   return y;
 }
 __device__ __forceinline__ f2 exp2_add(f2 x, f2 acc) {

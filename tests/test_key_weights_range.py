@@ -48,3 +48,39 @@ def test_rows_without_weight_may_hold_anything(mea, K, dtype, M, causal):
     for x in (math.nan, math.inf, -math.inf):
         got = mea.mea_key_weights(q.masked_fill(pad[:, :, None, None], x), k, lse, causal=causal)
         assert torch.equal(got, want)
+
+
+POWERS = [-300.0, -127.4, -126.6, -126.2, -125.9, -100.3, -1.5, -0.5, 0.0, 0.4999, 0.5, 0.7, 64.3, 126.4,
+          126.6, 127.3, 127.7, 128.4, 200.0, math.inf, -math.inf, math.nan]
+
+
+@pytest.mark.parametrize("K,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("M", [1, 256])
+def test_the_exponential_over_its_range(mea, K, dtype, M):
+    """One row's weight 2^x at every place of a tile (each takes one of two exponentials), all
+    other rows' at 2^-300.  Below the normal range the result may be 0; between 127.5 and 128
+    it may be infinite."""
+    H = min(M, 64)
+    x = torch.tensor(POWERS, dtype=torch.float64)
+    q = torch.zeros(len(POWERS), M, H, K, dtype=DT[dtype], device=DEV)
+    k = torch.zeros(len(POWERS), 256, H, K, dtype=DT[dtype], device=DEV)
+    lse = torch.full((len(POWERS), H, M), 300.0 * math.log(2))
+    for h in range(H):
+        lse[:, h, h * M // H] = (-x * math.log(2)).float()
+    w = mea.mea_key_weights(q, k, lse.to(DEV), causal=False).double().cpu()
+    for i, p in enumerate(POWERS):
+        exact = torch.exp(-lse[i, 0, 0].double())  # of the lse that fp32 holds
+        if math.isnan(p):
+            assert torch.isnan(w[i]).all()
+        elif p == math.inf:  # lse = -inf: a row without weight
+            assert (w[i] == 0).all()
+        elif exact >= 2.0 ** 128:
+            assert torch.isposinf(w[i]).all(), p
+        else:
+            # -lse log2(e) in fp32 (two roundings), exp2's 2^-21, and the subnormals
+            tol = exact * ((abs(p) + 1) * 2.0 ** -23 + 2.0 ** -21)
+            tol = tol if exact > 2.0 ** -125.5 else 2.0 ** -125.5
+            ok = (w[i] - exact).abs() <= tol
+            if exact > 2.0 ** 127.4:
+                ok |= torch.isposinf(w[i])
+            assert ok.all(), (p, w[i].min(), w[i].max(), exact)
