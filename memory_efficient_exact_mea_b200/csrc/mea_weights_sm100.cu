@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
     const int grp = warp >> 2, half = grp / C::kParity;
     const int key = n0 + half * kWeightKeys + (warp & 3) * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    f2 acc = {0.f, 0.f};
     const f2 sc2 = {a.scale_log2, a.scale_log2};
     for (int s = grp % C::kParity; s < steps; s += C::kParity) {
       const int g = (s_first + s) / mblocks, m0 = m_first + (s_first + s - g * mblocks) * NQ;
@@ -290,6 +289,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
       tc_fence_after();
       const float* lse = s_lse + ls * NQ;
       [[maybe_unused]] const float slope = ALIBI ? s_slope[ls] : 0.f;
+      f2 acc = {0.f, 0.f};  // of this tile: the total takes one term a tile, whatever M and G
       // `open`: every column of the tile counts for every key of it (rows past m have an
       // lse of -inf here; a row that takes no weight may hold anything, NaN too)
       auto add_tile = [&](auto open) {
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtas)
       if (seen && s_open[ls]) add_tile(std::true_type{});
       else add_tile(std::false_type{});
       mbar_arrive_warp(&l_empty[ls]);
+      sum += acc.x + acc.y;
     }
-    sum = acc.x + acc.y;
     if (grp % C::kParity == 1) s_sum[key - n0] = sum;
   }
   tc_fence_before();

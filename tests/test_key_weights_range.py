@@ -84,3 +84,19 @@ def test_the_exponential_over_its_range(mea, K, dtype, M):
             if exact > 2.0 ** 127.4:
                 ok |= torch.isposinf(w[i])
             assert ok.all(), (p, w[i].min(), w[i].max(), exact)
+
+
+@pytest.mark.parametrize("K,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("lse", [0.1, 2.0, 7.7])
+def test_sums_of_many_equal_terms(mea, K, dtype, lse):
+    """32768 equal weights a key: sums of 64 within a tile, then one term a tile and joined
+    parts: 64 + 128 + 8 additions of 2^-24 in a row at most, beside each weight's own
+    -lse log2(e) and exp2."""
+    M, G = 8192, 4
+    for N, H in ((4096, 10), (128, 1)):  # a CTA a key block, and clusters that share one
+        q = torch.zeros(1, M, G * H, K, dtype=DT[dtype], device=DEV)
+        k = torch.zeros(1, N, H, K, dtype=DT[dtype], device=DEV)
+        w = mea.mea_key_weights(q, k, torch.full((1, G * H, M), lse, device=DEV), causal=False)
+        exact = M * G * math.exp(-float(torch.tensor(lse)))
+        tol = exact * (200 * 2.0 ** -24 + (1.5 * lse + 1) * 2.0 ** -23 + 2.0 ** -21)
+        assert ((w.double() - exact).abs() <= tol).all(), (w.double() / exact - 1).abs().max()
