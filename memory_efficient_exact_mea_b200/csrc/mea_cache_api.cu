@@ -94,12 +94,15 @@ bool row_order(mea::RowOrder* o, int B, int M, int Hkv) {
   return true;
 }
 
-// mea_key_weights with at most this many query rows and (row, query head) pairs a kv
-// head goes to the kernel that reads K once with mma.sync.  8 x 8 heads x 8192 keys,
-// K = 128, us here / with 128-row tiles: one row 37 / 90 (one query head), 37 / 158
-// (four), 36 / 250 (eight); 64 pairs 57 / 90, 57 / 157, 55 / 249; 128 pairs 88 / 158
-// (32 rows x 4), 86 / 249.  Full tiles win once they are full.
-constexpr int kFewRows = 64, kFewColumns = 128;
+// mea_key_weights with fewer query rows than a tile has (128) goes to the kernel that reads
+// K once with mma.sync, as long as its (row, query head) pairs fit the 48 KB that a block
+// may use as it is: 176 pairs at K = 128, 336 at K = 64.  8 x 8 heads x 8192 keys, us here /
+// with 128-row tiles, K = 128: one head a kv head 52 / 86 (64 rows), 73 / 87 (100), 85 / 81
+// (128); two 85 / 108 (64), 101 / 107 (80); four 101 / 153 (40); eight 98 / 245 (20).
+// K = 64: one head 48 / 68 (100); two 78 / 85 (100), 94 / 75 (128); four 114 / 126 (80);
+// eight 112 / 212 (40).  (4 x 2 heads x 4096 keys, too few to fill the GPU: 9 / 9 with 64
+// rows, 13 / 9 with 100.)  Past the limit a tile a head is taken however few its rows.
+constexpr int kFewRows = 127, kFewBytes = 48 * 1024;
 
 // Splits of one decode call.  A split is a whole number of 128-row steps (four
 // warps of 32 rows); long enough that its partial state (K floats a head) and
@@ -348,8 +351,8 @@ int mea_key_weights(const void* q, const void* k, const float* lse, const int32_
   if (!a.status) return MEA_ERR_CUDA;
   a.group = Hq / Hkv;
   // Few (row, head) pairs to a key: the kernel that is bound by reading K.
-  L.few = M <= kFewRows && static_cast<int64_t>(M) * a.group <= kFewColumns && Hkv <= 65535 &&
-          B <= 65535;
+  L.few = M <= kFewRows && mea::few_row_bytes(static_cast<int64_t>(M) * a.group, K) <= kFewBytes &&
+          Hkv <= 65535 && B <= 65535;
   const bool bf16 = dtype == MEA_BF16;
   if (L.few) {
     const int64_t units = static_cast<int64_t>(B) * Hkv;

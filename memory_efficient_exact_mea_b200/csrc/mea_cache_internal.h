@@ -143,6 +143,18 @@ struct WeightLaunch {
   bool few;  // few query rows: K read once, mma.sync
 };
 
+// Shared memory of the few-row kernel: per (row, query head) pair, in blocks of 8, what its
+// column needs and its row of q.
+struct FewColumn {
+  float nl;     // -lse log2(e); -inf: takes no weight
+  float slope;  // ALiBi, log2 units
+  int pos;      // position of the row
+  int last;     // last key it sees
+};
+inline int64_t few_row_bytes(int64_t pairs, int head_dim) {
+  return (pairs + 7) / 8 * 8 * (static_cast<int64_t>(sizeof(FewColumn)) + 2 * head_dim);
+}
+
 cudaError_t launch_weights(const WeightLaunch& launch, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------

@@ -392,13 +392,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-struct FewColumn {  // of one (row, head) pair
-  float nl;     // -lse log2(e); -inf: takes no weight
-  float slope;  // ALiBi, log2 units
-  int pos;      // position of the row
-  int last;     // last key it sees
-};
-
 template <int D, bool BF16, bool ALIBI>
 __global__ void __launch_bounds__(kFewThreads, 4)
     weights_few_kernel(const WeightArgs a, const uint16_t* q, const uint16_t* k, bool causal,
@@ -506,7 +499,7 @@ template <int D, bool BF16>
 cudaError_t launch_few(const WeightLaunch& L, cudaStream_t stream) {
   const WeightArgs& a = L.args;
   const int blocks = (a.M * a.group + 7) / 8;
-  const int smem = blocks * (8 * static_cast<int>(sizeof(FewColumn)) + D / 32 * 32 * 16);
+  const int smem = static_cast<int>(few_row_bytes(static_cast<int64_t>(a.M) * a.group, D));
   const dim3 grid((a.N + a.few_chunk - 1) / a.few_chunk, a.Hkv, a.B);
   const uint16_t* q = static_cast<const uint16_t*>(L.q);
   const uint16_t* k = static_cast<const uint16_t*>(L.k);

@@ -5,6 +5,9 @@ import math
 import pytest
 import torch
 
+from test_key_weights import check
+from test_key_weights import randn as host_randn
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -100,3 +103,14 @@ def test_sums_of_many_equal_terms(mea, K, dtype, lse):
         exact = M * G * math.exp(-float(torch.tensor(lse)))
         tol = exact * (200 * 2.0 ** -24 + (1.5 * lse + 1) * 2.0 ** -23 + 2.0 ** -21)
         assert ((w.double() - exact).abs() <= tol).all(), (w.double() / exact - 1).abs().max()
+
+
+@pytest.mark.parametrize("K,dtype,rows", [
+    (128, "bf16", [(1, 127), (1, 128), (2, 88), (2, 89), (8, 22), (8, 23), (44, 4), (177, 1)]),
+    (64, "f16", [(1, 127), (2, 127), (3, 112), (4, 84), (4, 85), (16, 21), (16, 22), (337, 1)])])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_both_sides_of_the_few_row_rule(mea, K, dtype, rows, alibi):
+    """(heads a kv head, rows) at the last size of one kernel and the first of the other."""
+    for G, M in rows:
+        q, k = host_randn((2, M, G, K), dtype, 41), host_randn((2, 200 + M, 1, K), dtype, 42)
+        check(mea, q, k, [200, 7], [M, M - 1], alibi=alibi)
