@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from test_key_weights import check
+import kv4_util as U
+from test_key_weights import check, plain_lse
 from test_key_weights import randn as host_randn
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +115,17 @@ def test_both_sides_of_the_few_row_rule(mea, K, dtype, rows, alibi):
     for G, M in rows:
         q, k = host_randn((2, M, G, K), dtype, 41), host_randn((2, 200 + M, 1, K), dtype, 42)
         check(mea, q, k, [200, 7], [M, M - 1], alibi=alibi)
+
+
+@pytest.mark.parametrize("K,dtype,M,N,Hq,Hkv,causal", [
+    (128, "bf16", 700, 700, 8, 2, True), (64, "f16", 515, 600, 4, 4, False),
+    (128, "f16", 16, 900, 8, 2, True), (64, "bf16", 1500, 300, 6, 1, False)])
+def test_norm_of_the_error(mea, K, dtype, M, N, Hq, Hkv, causal):
+    """Relative error in norm.  A product q.k is summed 16 terms at a time, each partial sum
+    (at most 64 for these inputs) cut at 2^-24 of itself: K/16 64 2^-23 / sqrt(K), 5.4e-6 at
+    K = 128; the score's scaling against lse, 2 x 2^-24 of 20; exp2 2^-21.  2^-16 holds them."""
+    q, k = host_randn((2, M, Hq, K), dtype, 51), host_randn((2, N, Hkv, K), dtype, 52)
+    lse = plain_lse(q, k, None, None, causal, K ** -0.5, False)
+    got = mea.mea_key_weights(q.to(DEV), k.to(DEV), lse.to(DEV), causal=causal).double().cpu()
+    want, _ = U.key_weights(q, k, lse, None, None, causal, K ** -0.5)
+    assert float((got - want).norm() / want.norm()) <= 2.0 ** -16
