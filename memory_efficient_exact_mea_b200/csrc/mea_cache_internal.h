@@ -48,7 +48,8 @@ bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int batch, int r
 // ---------------------------------------------------------------------------
 // 4-bit cache (mea_kv4_sm100.cu): planes [B, Hkv, cap, ...], contiguous.
 // ---------------------------------------------------------------------------
-// x / d for x < 2^31: (hi32(x m) + x) >> s.
+// x / d for x < 2^31: (hi32(x m) + x) >> s (division by an invariant through a
+// multiplication; Granlund and Montgomery, 1994).
 struct FastDiv {
   uint32_t d, m, s;
 };

@@ -71,24 +71,27 @@ __device__ __forceinline__ unsigned divide(unsigned x, const FastDiv& d) {
 // to d / s (in one fused step, d = x - z) rounds it to an integer in the low mantissa
 // bits; that is right unless the quotient lies next to a half.  There the sign of
 // x - (z + s (k + 1/2)) decides: s (k + 1/2) has at most 16 bits, d lies within a
-// factor of two of it, and the part of x - z that d lost is known, so the sign is
-// exact in fp32.
+// factor of two of it, and the part of x - z that d lost is known (the error term of
+// Knuth's two-sum), so the sign is exact.
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 
-__device__ __forceinline__ float code_near_half(float x, float z, float s, float inv) {
-  const float d = x - z;
-  const float bb = d - x;
-  const float lost = (x - (d - bb)) + (-z - bb);  // x - z = d + lost
-  const float q = d * inv;
-  const float k = floorf(q);
-  if (fabsf(q - k - 0.5f) > 1e-3f) return rintf(q);
-  const float over = (d - s * (k + 0.5f)) + lost;
-  return over > 0.f ? k + 1.f : over < 0.f ? k : rintf(k + 0.5f);
+// In fp32 with q = d / s to within 1e-4; in doubles (q = d / s) for steps outside
+// [2^-100, 2^100], where fp32's products could leave its range.
+template <typename T>
+__device__ __forceinline__ float code_near_half(T x, T z, T s, T inv) {
+  const T d = x - z;
+  const T bb = d - x;
+  const T lost = (x - (d - bb)) + (-z - bb);  // x - z = d + lost
+  T q;
+  if constexpr (sizeof(T) == 8) q = d / s;
+  else q = d * inv;
+  const T k = floor(q);
+  if (fabs(q - k - T(0.5)) > T(1e-3)) return static_cast<float>(rint(q));
+  const T over = (d - s * (k + T(0.5))) + lost;
+  return static_cast<float>(over > 0 ? k + 1 : over < 0 ? k : rint(k + T(0.5)));
 }
-
-// Steps outside [2^-100, 2^100]: the same in doubles.
 __device__ __noinline__ float code_wide(float x, float z, float s) {
-  return static_cast<float>(rint((static_cast<double>(x) - z) / s));
+  return code_near_half<double>(x, z, s, 0.0);
 }
 
 // Packed minimum and maximum; a NaN stays one.
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) kv4_append_kernel(const Kv4App
           const float m = fminf(fmaf(d, inv, kRound), kRound + 15.f);
           if (fabsf(fmaf(d, inv, kRound - m)) > 0.4999f) {
             const uint32_t c =
-                static_cast<uint32_t>(fminf(code_near_half(x[i], z, s, inv), 15.f));
+                static_cast<uint32_t>(fminf(code_near_half<float>(x[i], z, s, inv), 15.f));
             word = (word & ~(15u << (4 * i))) | (c << (4 * i));
           }
         }

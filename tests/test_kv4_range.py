@@ -1,6 +1,7 @@
 """The 4-bit decode over its whole range of values: groups of very different size, values
 near the ends of the type, and every row's place in the result (bounds in kv4_bounds)."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -191,6 +192,26 @@ def test_the_largest_numbers_stay_finite(mea, dtype):
         assert ((got - want).abs() <= tol)[:5].all()
     # the listed top itself comes back
     assert (k[0, 0, 0, 7] == top).item() and (k[1, 0, 0, 0] == top).item()
+
+
+@pytest.mark.parametrize("dtype,step", [("bf16", 101), ("bf16", 110), ("bf16", 20), ("bf16", -101),
+                                        ("bf16", -118), ("f16", 2), ("f16", -5)])
+@pytest.mark.parametrize("least", [-1.0, 0.0, 1.0])
+def test_codes_beside_a_tie(mea, dtype, step, least):
+    """Values at halves of steps above zero, the group's least value a hair off zero (so far
+    below them that a difference of the two may round it away): fractions decide the codes."""
+    dt = DT[dtype]
+    hair = torch.finfo(dt).smallest_normal if step > 0 else torch.finfo(dt).tiny / 64
+    s = 2.0 ** step
+    x = torch.tensor([least * hair] + [s * i / 2 for i in range(31)] + [s * 15.0] * 32)
+    x = x.clamp_min(least * hair).to(dt)
+    cache = filled(mea, *[x.view(1, 1, 1, 64)] * 2, [1])
+    param = cache.k_params[0, 0, 0, 0].double().tolist()
+    fs, fz = Fraction(param[0]), Fraction(param[1])
+    assert fs == Fraction(s) and fz == Fraction(float(x.double().min()))
+    want = [min(15, max(0, round((Fraction(float(t)) - fz) / fs))) for t in x.double()]  # ties to even
+    got = cache.k_codes[0, 0, 0].cpu()
+    assert torch.stack((got & 15, got >> 4), -1).flatten().tolist() == want
 
 
 PROBES = [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 1000, 1535, 1536, 1537, 2047, 2048, 4095, 4096,
