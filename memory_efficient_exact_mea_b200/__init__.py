@@ -646,7 +646,7 @@ def mea_decode_kv4(q, cache: Kv4Cache, kv_seqlens, max_kv_len: int, scale: float
     _on(index, q, "q")
     _on_stream(index, stream)
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _empty(shape, dtype, q.device, stream)
     elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped and typed like q")
     if lse is not None:
