@@ -377,8 +377,9 @@ int mea_kv4_read(const void* k_codes, const void* k_params, const void* v_codes,
 /*
  * mea_decode_kv4 -- mea_decode on a 4-bit cache: a single new query per sequence
  * against rows [0, kv_seqlens[b]) of its slot (the new token's row already
- * appended), with the values the codes stand for; no value of the cache is rounded
- * again on the way.
+ * appended), with the values the codes stand for: codes, steps and zeros go in as they
+ * are held, each softmax weight times a step as two fp16 parts (off by at most 2^-22 of
+ * itself or 2^-28 of the largest such product of the group), the sums in fp32.
  *   q, out       [B, Hq, K] contiguous, dtype (the type the cache was stored with)
  *   lse          [B, Hq] fp32 natural log, or NULL
  *   kv_seqlens   DEVICE int32 [B]

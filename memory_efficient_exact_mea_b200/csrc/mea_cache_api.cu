@@ -108,8 +108,8 @@ constexpr int kFewRows = 127, kFewBytes = 48 * 1024;
 // warps of 32 rows); long enough that its partial state (K floats a head) and
 // its start-up stay small beside the rows it reads, short enough that the grid
 // fills the GPU's resident CTAs a few times over: at most 768 / 1024 / 1536 / 2048
-// rows took 82.7 / 79.5 / 78.1 / 79.6 us for 64 sequences of up to 8192 rows and
-// 67.0 / 64.0 / 63.1 / 64.6 us for four of up to 65521.
+// rows took 94.1 / 88.7 / 84.5 / 83.7 us for 64 sequences of up to 8192 rows and
+// 91.2 / 85.1 / 82.2 / 81.6 us for four of up to 65521.
 struct DecodePlan {
   int head_blocks, chunk, splits;
 };
@@ -120,7 +120,7 @@ DecodePlan decode_plan(int B, int Hq, int Hkv, int max_len) {
   const int64_t units = static_cast<int64_t>(B) * Hkv * p.head_blocks;
   const int64_t want = std::max<int64_t>(1, 148 * 6 / std::max<int64_t>(1, units));
   int64_t chunk = (max_len + want - 1) / want;
-  chunk = std::min<int64_t>(1536, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
+  chunk = std::min<int64_t>(2048, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
   chunk = std::max<int64_t>(chunk, ((max_len + int64_t(65534)) / 65535 + 127) / 128 * 128);
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((static_cast<int64_t>(max_len) + chunk - 1) / chunk);

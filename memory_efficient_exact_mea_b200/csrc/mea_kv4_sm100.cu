@@ -346,16 +346,15 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 //
 // Both products run in fp16 whatever the input type.  q is scaled by a power of two to
 // a largest magnitude below 256, exact but for values 2^-22 of that and less.
-// P' = p s goes in as two fp16 numbers, high and low (22 bits): with one, a fifth of the
-// bf16 results of the B = 64 decode differed from those of fp32 weights (2 % with two),
-// at 79 instead of 84 us.  p = 2^(y - ref) with ref
-// the running maximum of a head's scores; what goes in is p s F, F a power of two for
-// each (head, group of 64 dimensions) that puts the largest p s so far at 2^4, so that
-// a group keeps its bits however small its steps are beside the other group's.  fp16's
-// range then ends 28 powers of two below a group's largest p s; a row that far below
-// adds less than the sum's own rounding.  ref and F move only when some p s F passes
-// 2^15 or some p 2^11 (so the accumulators are rarely rescaled), or when p z F, kept in
-// fp32, passes 2^100.
+// p s goes in as two fp16 numbers, high and low (22 bits): with one, a fifth of the bf16
+// results of the B = 64 decode differed from those of fp32 weights (2 % with two), at
+// 79 instead of 84 us.  p = 2^(y - ref), ref the running maximum of a head's scores; what
+// goes in is p s F, F a power of two for each (head, group of 64 dimensions) that puts
+// the largest p s so far at 2^4, so that a group keeps its bits however small its steps
+// are beside the other group's.  fp16's range then ends 28 powers of two below a group's
+// largest p s; a row that far below adds less than the sum's own rounding.  ref and F
+// move only when some p s F passes 2^15 or some p 2^11 (so the accumulators are rarely
+// rescaled), or when p z F, kept in fp32, passes 2^100.
 //
 // A warp takes 32 rows at a time in the fragment layout of mma.sync m16n8k16 (rows
 // x heads and dimensions x heads, heads padded to 8): a thread's nibbles for one
@@ -1096,8 +1095,8 @@ template <int D, bool BF16>
 cudaError_t decode_t(const Kv4DecodeArgs& a, bool alibi, cudaStream_t stream) {
   if (a.max_splits > 0) {
     const dim3 grid(a.Hkv * a.head_blocks, a.B, a.max_splits);
-    // Up to four heads at K = 128: a column for each (group, head) (78 us at B = 64,
-    // 63 us for four long contexts; without, 81 and 69 us).
+    // Up to four heads at K = 128: a column for each (group, head) (84 us at B = 64,
+    // 82 us for four long contexts with weights; without, 96 and 90 us).
     cudaError_t e;
     if (D == 128 && a.group <= 4)
       e = alibi ? decode_run<D, BF16, true, D == 128>(a, grid, stream)

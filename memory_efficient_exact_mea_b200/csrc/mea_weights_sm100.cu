@@ -11,7 +11,7 @@
 // thread's own row -- no reduction across lanes, no atomics, the same order every
 // time.  For each 128 keys, two groups of four warps take alternate tiles (one TMEM
 // buffer each), so one group's exponentials overlap the other's MMA and TMEM read.
-// Bound by the exponential unit (16 a clock per SM; 75 % busy at K = 128).
+// Bound by the exponential unit (16 a clock per SM; 74 % busy at K = 128, 71 % at 64).
 //
 // A few query rows (a decode step, a short chunk) go to weights_few_kernel: the same
 // sum with mma.sync straight from global memory, bound by reading K once.
@@ -61,9 +61,9 @@ __device__ __forceinline__ f2 exp2_add(f2 x, f2 acc) {
   return fma2(p, two_n, acc);
 }
 
-// Which of a chunk's 16 pairs take the polynomial, spread evenly: the exponential
-// unit alone measured 372 / 178 us (causal 4 x 4096, two-sided 8 x 2048), 3 of 16
-// pairs here 349 / 164 us, 5 of 16 358 / 167 us.
+// Which of a chunk's 16 pairs take the polynomial, spread evenly: 0 / 2 / 3 / 4 / 5 of 16
+// measured 350 / 330 / 325 / 328 / 334 us (causal 4 x 4096) and 168 / 157 / 153 / 153 /
+// 153 us (two-sided 8 x 2048).
 constexpr int kPolyOf16 = 3;
 __device__ __forceinline__ constexpr bool on_fma_pipe(int pair) {
   return (pair * kPolyOf16) % 16 < kPolyOf16;
